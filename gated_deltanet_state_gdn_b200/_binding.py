@@ -32,6 +32,7 @@ GDN_ERR_CUDA = 7
 GDN_F32 = 0
 GDN_BF16 = 1
 GDN_F16 = 2
+GDN_E4M3 = 3
 
 GDN_PREFILL_SEQUENTIAL = 1
 GDN_DISABLE_STATE_UPDATE = 2
@@ -43,6 +44,7 @@ GDN_RULE_LINEAR = 3 << 3
 GDN_GATE_QWEN = 1 << 5
 GDN_BETA_SIGMOID = 1 << 6
 GDN_DECAY_PER_KEY = 1 << 8
+GDN_ZERO_PADDING = 1 << 9
 
 # update_rule of the op -> (flag bits, has decay input, has beta input)
 UPDATE_RULES = {
@@ -56,11 +58,17 @@ GDN_DEV_BAD_SLOT = 1
 GDN_DEV_TIMEOUT = 2
 GDN_DEV_INTERNAL = 4
 GDN_DEV_BOUNDS = 8            # checked builds only
+GDN_DEV_BAD_PAGE = 16
+GDN_DEV_BAD_LENGTH = 32
+GDN_DEV_CONFLICT = 64
+GDN_DEV_NO_PAGES = 128
 GDN_DEV_TEST_STALL = 1 << 30  # checked builds only, set by the caller (decode timeout path)
 
 EXPORTED = ("gdn_prefill", "gdn_prefill_ws", "gdn_prefill_workspace_size",
             "gdn_prefill_noalloc", "gdn_decode", "gdn_conv1d", "gdn_status_string",
-            "gdn_last_error", "gdn_abi_version", "gdn_prefill_uses_chunked")
+            "gdn_last_error", "gdn_abi_version", "gdn_prefill_uses_chunked", "gdn_kv_append",
+           "gdn_paged_attn", "gdn_paged_attn_workspace_size", "gdn_page_resize", "gdn_page_fork",
+           "gdn_page_compact", "gdn_page_workspace_size")
 
 _lib = None
 
@@ -123,6 +131,23 @@ def lib():
         L.gdn_abi_version.argtypes = []
         L.gdn_prefill_uses_chunked.restype = i32
         L.gdn_prefill_uses_chunked.argtypes = [ctypes.c_int, i32, i32, i32, u32]
+        u64 = ctypes.c_uint64
+        L.gdn_kv_append.restype = ctypes.c_int
+        L.gdn_kv_append.argtypes = [vp, vp, i64, i64, i64, i64, vp, vp, vp, i32, i64,
+                                    ctypes.c_int, vp, vp]
+        L.gdn_paged_attn.restype = ctypes.c_int
+        L.gdn_paged_attn.argtypes = [vp, i64, i64, vp, vp, i32, i32, i32, ctypes.c_int, f32, i32,
+                                     vp, vp, u32, vp, u64, vp, vp]
+        L.gdn_paged_attn_workspace_size.restype = u64
+        L.gdn_paged_attn_workspace_size.argtypes = [i32, i32, i32, i32, i32, ctypes.c_int]
+        L.gdn_page_resize.restype = ctypes.c_int
+        L.gdn_page_resize.argtypes = [vp, vp, vp, i32, vp, i32, vp, u64, vp, vp]
+        L.gdn_page_fork.restype = ctypes.c_int
+        L.gdn_page_fork.argtypes = [vp, vp, vp, i32, vp, i32, vp, vp]
+        L.gdn_page_compact.restype = ctypes.c_int
+        L.gdn_page_compact.argtypes = [vp, vp, vp, i32, vp, u64, vp, vp]
+        L.gdn_page_workspace_size.restype = u64
+        L.gdn_page_workspace_size.argtypes = [i32, i32]
         _lib = L
     return _lib
 

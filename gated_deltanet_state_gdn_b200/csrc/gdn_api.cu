@@ -7,6 +7,7 @@
 #include <string.h>
 
 #include "common.cuh"
+#include "host_checks.cuh"
 
 namespace {
 
@@ -19,18 +20,10 @@ gdn_status cuda_fail(cudaError_t e, const char *where)
     return GDN_ERR_CUDA;
 }
 
-bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
-
-// [p, p + bytes) and [q, q + qbytes) intersect (both non-empty)
-bool overlaps(const void *p, size_t bytes, const void *q, size_t qbytes)
-{
-    if (!p || !q || bytes == 0 || qbytes == 0) return false;
-    uintptr_t a0 = (uintptr_t)p, a1 = a0 + bytes;
-    uintptr_t b0 = (uintptr_t)q, b1 = b0 + qbytes;
-    return a0 < b1 && b0 < a1;
-}
-
 }  // namespace
+
+using gdn::aligned;
+using gdn::overlaps;
 
 gdn_status gdn_report_cuda_failure(cudaError_t e, const char *where) { return cuda_fail(e, where); }
 

@@ -1,0 +1,581 @@
+// pages.cu -- the page table of the paged cache: growing, shrinking, forking and compacting its
+// rows, with the copies of pages and states that follow.
+//
+// The tables are integers of a few megabytes at most; a call's time is the latency of its
+// dependent steps.  Resize and compact run them in one cluster of eight blocks, whose barrier
+// orders the steps (about a microsecond each where a launch a step would cost two to three).
+// The copies are HBM-bound (each byte read once and written once) and run in a second kernel
+// over the whole GPU, brought up while the first one drains.  Everything is decided by scans in
+// the order of the lists and of the page numbers, so a call has one result; atomics only count
+// integers.
+#include <cooperative_groups.h>
+
+#include "cache.cuh"
+
+namespace gdn_pages {
+
+namespace cg = cooperative_groups;
+using namespace gdn_cache;
+using gdn::in_range;
+
+constexpr int kCluster = 8;
+constexpr int kThreads = 1024;          // of a planning block
+constexpr int kWarps = kCluster * kThreads / 32;
+constexpr int kChunk = 128;             // table entries a warp takes at a time
+constexpr int kCopyThreads = 256;
+constexpr int kCopyBytes = 16384;       // of a row a block copies at a time
+constexpr int kMaxPools = 96;           // a launch (a kernel's arguments hold 4 KB)
+
+struct Pool {
+    unsigned char *data;
+    int64_t stride, bytes;
+    int first, width;                   // first piece of a row among all pools'; access width
+};
+struct Pools {
+    Pool p[kMaxPools];
+    int n, pieces;                      // pieces of a row over all pools
+};
+
+struct alignas(16) Row {                // what resize does to a listed row
+    int row, had, want, first;          // pages before and after; first new page's place
+    int len, copied, last, pad;         // new length; a shared page is replaced; that page
+};
+
+__device__ __forceinline__ void tell(int32_t *status, int bit)
+{
+    if (status) atomicOr(status, bit);
+}
+
+__device__ __forceinline__ int pages_of(int len, int page) { return (int)(((int64_t)len + page - 1) / page); }
+
+__device__ __forceinline__ bool length_ok(const gdn_page_table &t, int len)
+{
+    return len >= 0 && len <= (int64_t)t.width * t.page_size;
+}
+
+// exclusive prefix sum over the block's threads; *total is the same in all
+__device__ __forceinline__ int block_scan(int x, int *s_warp, int *total)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    int incl = x;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += y;
+    }
+    if (lane == 31) s_warp[warp] = incl;
+    __syncthreads();
+    int w = lane < nw ? s_warp[lane] : 0, wi = w;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, wi, d);
+        if (lane >= d) wi += y;
+    }
+    const int before = __shfl_sync(0xffffffffu, wi - w, warp);
+    *total = __shfl_sync(0xffffffffu, wi, 31);
+    __syncthreads();                    // s_warp is used again
+    return before + incl - x;
+}
+
+// copy piece `item` of row src to row dst
+__device__ __forceinline__ void copy_piece(const Pools &ps, int item, int64_t src, int64_t dst)
+{
+    int lo = 0, hi = ps.n - 1;          // the last pool whose first piece is <= item
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (ps.p[mid].first <= item) lo = mid; else hi = mid - 1;
+    }
+    const Pool &p = ps.p[lo];
+    const int64_t at = (int64_t)(item - p.first) * kCopyBytes;
+    const int64_t n = p.bytes - at < kCopyBytes ? p.bytes - at : kCopyBytes;
+    const unsigned char *const s = p.data + src * p.stride + at;
+    unsigned char *const d = p.data + dst * p.stride + at;
+    const int tid = threadIdx.x;
+    if (p.width == 16) {
+        constexpr int kHold = kCopyBytes / 16 / kCopyThreads;
+        const uint4 *const s16 = reinterpret_cast<const uint4 *>(s);
+        uint4 *const d16 = reinterpret_cast<uint4 *>(d);
+        const int w = (int)(n / 16);
+        uint4 x[kHold];
+#pragma unroll
+        for (int k = 0; k < kHold; ++k)
+            if (tid + k * kCopyThreads < w) x[k] = __ldcs(s16 + tid + k * kCopyThreads);
+#pragma unroll
+        for (int k = 0; k < kHold; ++k)
+            if (tid + k * kCopyThreads < w) __stcs(d16 + tid + k * kCopyThreads, x[k]);
+    } else if (p.width == 4) {
+        const uint32_t *const s4 = reinterpret_cast<const uint32_t *>(s);
+        for (int i = tid; i < (int)(n / 4); i += kCopyThreads) reinterpret_cast<uint32_t *>(d)[i] = __ldcs(s4 + i);
+    } else if (p.width == 2) {
+        const uint16_t *const s2 = reinterpret_cast<const uint16_t *>(s);
+        for (int i = tid; i < (int)(n / 2); i += kCopyThreads) reinterpret_cast<uint16_t *>(d)[i] = __ldcs(s2 + i);
+    } else {
+        for (int i = tid; i < (int)n; i += kCopyThreads) d[i] = __ldcs(s + i);
+    }
+}
+
+// The copies that a plan wrote down: pairs[k] = (src, dst), disjoint.  With a table, its entries
+// are first renamed by `map` (compact).
+__global__ void __launch_bounds__(kCopyThreads)
+copy_pairs_kernel(const __grid_constant__ Pools ps, const int2 *pairs, const int *count,
+                  const int num_rows, const gdn_page_table t, const int32_t *map, int32_t *status)
+{
+    wait_primary();
+    const int n = *count;
+    if (map) {
+        const int64_t words = (int64_t)t.rows * t.width;
+        for (int64_t i = (int64_t)blockIdx.x * kCopyThreads + threadIdx.x; i < words;
+             i += (int64_t)gridDim.x * kCopyThreads) {
+            const int s = (int)(i / t.width), j = (int)(i - (int64_t)s * t.width);
+            const int len = __ldg(t.seq_lens + s);
+            if (!length_ok(t, len)) {
+                if (j == 0) tell(status, GDN_DEV_BAD_LENGTH);
+                continue;
+            }
+            if (j >= pages_of(len, t.page_size)) continue;
+            int32_t *const e = t.block_table + s * t.table_stride + j;
+            const int id = *e;
+            const int to = (uint32_t)id < (uint32_t)t.num_pages ? __ldcg(map + id) : -1;
+            if (to < 0)
+                tell(status, GDN_DEV_BAD_PAGE);
+            else if (to != id)
+                *e = to;
+        }
+    }
+    const int64_t items = (int64_t)n * ps.pieces;
+    for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
+        const int2 p = pairs[i / ps.pieces];
+        if (in_range(p.x, 1, num_rows, status) && in_range(p.y, 1, num_rows, status))
+            copy_piece(ps, (int)(i % ps.pieces), p.x, p.y);
+    }
+}
+
+// ------------------------------------------------------------------ resize
+// Workspace: count | pairs [n] | a copy of the rows for each block [8][n] | free pages [P]
+struct ResizeWork {
+    int *count;
+    int2 *pairs;
+    Row *rows;
+    int *free_list;
+};
+
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
+resize_kernel(const gdn_page_table t, const int32_t *row_list, const int32_t *new_lens, const int n,
+              const ResizeWork ws, int32_t *status)
+{
+    cg::cluster_group cluster = cg::this_cluster();
+    const int rank = (int)cluster.block_rank(), tid = threadIdx.x, lane = tid & 31;
+    const int gw = (tid >> 5) * kCluster + rank;       // warp of the cluster
+    __shared__ int s_list[kThreads];
+    __shared__ int s_warp[32];
+    __shared__ int s_most[2];
+    __shared__ int s_free;
+    Row *const rows = ws.rows + (int64_t)rank * n;
+    launch_dependents();
+
+    // 1. what is asked of each row (every block works it out for itself)
+    if (tid == 0) s_most[0] = s_most[1] = 0;
+    for (int i0 = 0; i0 < n; i0 += kThreads) {
+        const int i = i0 + tid;
+        const int r = i < n ? __ldg(row_list + i) : -1;
+        int twice = 0;
+        for (int k0 = 0; k0 < n; k0 += kThreads) {
+            __syncthreads();
+            s_list[tid] = k0 + tid < n ? __ldg(row_list + k0 + tid) : -1;
+            __syncthreads();
+            const int most = min(kThreads, n - k0);
+            for (int k = 0; k < most; ++k) twice += s_list[k] == r;
+        }
+        if (i >= n) continue;
+        Row x = {-1, 0, 0, 0, 0, 0, 0, 0};
+        int bad = 0;
+        if (r >= t.rows) {
+            bad = GDN_DEV_BAD_SLOT;
+        } else if (r >= 0) {
+            const int old = __ldcg(t.seq_lens + r), len = __ldg(new_lens + i);
+            if (twice > 1) {
+                bad = GDN_DEV_CONFLICT;
+            } else if (!length_ok(t, old) || !length_ok(t, len)) {
+                bad = GDN_DEV_BAD_LENGTH;
+            } else {
+                x.row = r;
+                x.had = pages_of(old, t.page_size);
+                x.want = pages_of(len, t.page_size);
+                x.len = len;
+                x.copied = len > old && old % t.page_size != 0;   // until the count is seen
+                if (x.had > x.want) atomicMax(&s_most[0], x.had - x.want);
+                if (x.want > x.had || x.copied) atomicMax(&s_most[1], x.want - x.had + 1);
+            }
+        }
+        if (bad && rank == 0) tell(status, bad);
+        rows[i] = x;
+    }
+    __syncthreads();
+    const int most_gone = s_most[0], most_new = s_most[1];
+
+    // 2. pages past the new lengths go back; a warp takes kChunk entries of a row at a time
+    const int64_t gone_units = (int64_t)((most_gone + kChunk - 1) / kChunk) * n;
+    for (int64_t u = gw; u < gone_units; u += kWarps) {
+        const Row x = rows[u % n];
+        const int j0 = x.want + (int)(u / n) * kChunk;
+        if (x.row < 0 || j0 >= x.had) continue;
+        int32_t *const e = t.block_table + x.row * t.table_stride;
+        int id[kChunk / 32];
+#pragma unroll
+        for (int k = 0; k < kChunk / 32; ++k) {
+            const int j = j0 + k * 32 + lane;
+            id[k] = j < x.had && in_range(j, 1, t.width, status) ? e[j] : -2;
+        }
+#pragma unroll
+        for (int k = 0; k < kChunk / 32; ++k) {
+            if (id[k] == -2 && j0 + k * 32 + lane >= x.had) continue;
+            if ((uint32_t)id[k] < (uint32_t)t.num_pages)
+                atomicSub(t.ref_count + id[k], 1);
+            else
+                tell(status, GDN_DEV_BAD_PAGE);
+            e[j0 + k * 32 + lane] = -1;
+        }
+    }
+    cluster.sync();
+
+    // 3. how many pages each row takes, and where its share begins (every block for itself)
+    int total = 0, copies = 0;
+    if (most_new > 0) {
+        for (int i0 = 0; i0 < n; i0 += kThreads) {
+            const int i = i0 + tid;
+            int need = 0;
+            Row x;
+            if (i < n) {
+                x = rows[i];
+                if (x.row >= 0 && x.copied) {
+                    x.last = __ldcg(t.block_table + x.row * t.table_stride + x.had - 1);
+                    if ((uint32_t)x.last >= (uint32_t)t.num_pages) {
+                        if (rank == 0) tell(status, GDN_DEV_BAD_PAGE);
+                        x.row = -1;
+                    } else {
+                        x.copied = __ldcg(t.ref_count + x.last) > 1;
+                    }
+                }
+                if (x.row >= 0) need = max(x.want - x.had, 0) + x.copied;
+            }
+            int sum;
+            const int before = block_scan(need, s_warp, &sum);
+            if (i < n) {
+                x.first = total + before;
+                x.pad = need;
+                rows[i] = x;
+            }
+            total += sum;
+        }
+    }
+
+    // 4. the lowest free pages, in order: each block counts its share of the pages, the counts
+    //    are exchanged, then it writes its part of the list
+    int free_all = 0;
+    if (total > 0) {
+        const int share = ((t.num_pages + kCluster - 1) / kCluster + 3) / 4 * 4;
+        const int p0 = min(rank * share, t.num_pages), p1 = min(p0 + share, t.num_pages);
+        int mine = 0;
+#pragma unroll 4
+        for (int p = p0 + tid; p < p1; p += kThreads) mine += __ldcg(t.ref_count + p) <= 0;
+        int sum;
+        block_scan(mine, s_warp, &sum);
+        if (tid == 0) s_free = sum;
+        cluster.sync();
+        int at = 0;
+        for (int k = 0; k < kCluster; ++k) {
+            const int f = *cluster.map_shared_rank(&s_free, k);
+            if (k < rank) at += f;
+            free_all += f;
+        }
+        for (int p = p0; p < p1 && at < total; p += kThreads) {
+            const bool is = p + tid < p1 && __ldcg(t.ref_count + p + tid) <= 0;
+            const int k = at + block_scan(is, s_warp, &sum);
+            if (is && k < total && in_range(k, 1, t.num_pages, status)) ws.free_list[k] = p + tid;
+            at += sum;
+        }
+    }
+    cluster.sync();
+
+    // 5. rows that fit take their pages
+    for (int i0 = 0; i0 < n; i0 += kThreads) {
+        const int i = i0 + tid;
+        int copy = 0;
+        Row x;
+        if (i < n) {
+            x = rows[i];
+            if (x.row >= 0 && x.pad > 0 && x.first + x.pad > free_all) {
+                if (rank == 0) tell(status, GDN_DEV_NO_PAGES);
+                rows[i].row = x.row = -1;
+            }
+            copy = x.row >= 0 && x.pad > 0 && x.copied;
+        }
+        int sum;
+        const int k = copies + block_scan(copy, s_warp, &sum);
+        copies += sum;
+        if (rank == 0 && i < n && x.row >= 0) {
+            t.seq_lens[x.row] = x.len;
+            if (copy) {
+                atomicSub(t.ref_count + x.last, 1);
+                ws.pairs[k] = make_int2(x.last, ws.free_list[x.first]);
+            }
+        }
+    }
+    if (rank == 0 && tid == 0) *ws.count = copies;
+    __syncthreads();
+    const int64_t new_units = total > 0 ? (int64_t)((most_new + kChunk - 1) / kChunk) * n : 0;
+    for (int64_t u = gw; u < new_units; u += kWarps) {
+        const Row x = rows[u % n];
+        if (x.row < 0 || x.pad == 0) continue;
+        const int from = x.had - x.copied;        // the entry that gets the row's first page
+        const int j0 = (int)(u / n) * kChunk;
+#pragma unroll
+        for (int k = 0; k < kChunk / 32; ++k) {
+            const int j = j0 + k * 32 + lane;
+            if (j >= x.pad || !in_range(from + j, 1, t.width, status)) continue;
+            const int id = ws.free_list[x.first + j];
+            t.block_table[x.row * t.table_stride + from + j] = id;
+            t.ref_count[id] = 1;
+        }
+    }
+    cluster.sync();      // no block leaves while another may read its shared memory
+}
+
+// ------------------------------------------------------------------ compact
+// Workspace: count, rank of page U | pairs [P] | used pages by rank [P] | free pages by rank [P]
+struct CompactWork {
+    int *count;
+    int2 *pairs;
+    int *used, *open;
+};
+
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
+compact_kernel(const gdn_page_table t, int32_t *const map, const CompactWork ws, int32_t *status)
+{
+    cg::cluster_group cluster = cg::this_cluster();
+    const int rank = (int)cluster.block_rank(), tid = threadIdx.x;
+    __shared__ int s_warp[32];
+    __shared__ int s_used;
+    launch_dependents();
+    const int P = t.num_pages;
+    const int share = ((P + kCluster - 1) / kCluster + 3) / 4 * 4;
+    const int p0 = min(rank * share, P), p1 = min(p0 + share, P);
+    int mine = 0, sum;
+#pragma unroll 4
+    for (int p = p0 + tid; p < p1; p += kThreads) mine += __ldcg(t.ref_count + p) > 0;
+    block_scan(mine, s_warp, &sum);
+    if (tid == 0) s_used = sum;
+    cluster.sync();
+    int at = 0, U = 0;
+    for (int k = 0; k < kCluster; ++k) {
+        const int f = *cluster.map_shared_rank(&s_used, k);
+        if (k < rank) at += f;
+        U += f;
+    }
+    // Of the pages in order, `at` are used before p.  A used page of number >= U is the
+    // (at - used before U)-th to move, a free one below U the (p - at)-th place.
+    for (int p = p0; p < p1; p += kThreads) {
+        const int q = p + tid;
+        const bool in = q < p1, is = in && __ldcg(t.ref_count + q) > 0;
+        const int k = at + block_scan(is, s_warp, &sum);
+        at += sum;
+        if (!in) continue;
+        if (q == U) ws.count[1] = k;
+        map[q] = is ? q : -1;
+        if (is && q >= U && in_range(k, 1, P, status)) ws.used[k] = q;
+        if (!is && q < U && in_range(q - k, 1, P, status)) ws.open[q - k] = q;
+    }
+    cluster.sync();
+    const int below = U < P ? __ldcg(ws.count + 1) : U;     // used pages of number < U
+    const int moves = U - below;
+    for (int k = rank * kThreads + tid; k < moves; k += kCluster * kThreads) {
+        const int src = __ldcg(ws.used + below + k), dst = __ldcg(ws.open + k);
+        t.ref_count[dst] = __ldcg(t.ref_count + src);
+        t.ref_count[src] = 0;
+        map[src] = dst;
+        ws.pairs[k] = make_int2(src, dst);
+    }
+    if (rank == 0 && tid == 0) ws.count[0] = moves;
+    cluster.sync();      // no block leaves while another may read its shared memory
+}
+
+// ------------------------------------------------------------------ fork
+// Blocks [0, n) rename table rows, the others copy pieces of the pools.  Which pairs stand
+// depends on the two lists alone, so every block checks its own pair.
+__global__ void __launch_bounds__(kCopyThreads)
+fork_kernel(const __grid_constant__ Pools ps, const gdn_page_table t, const int32_t *parents,
+            const int32_t *children, const int n, const int table_blocks, int32_t *status)
+{
+    const int tid = threadIdx.x;
+    const int64_t items = table_blocks + (int64_t)n * ps.pieces;
+    for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
+        const bool table = i < table_blocks;
+        const int k = table ? (int)i : (int)((i - table_blocks) / ps.pieces);
+        const int p = __ldg(parents + k), c = __ldg(children + k);
+        if (p < 0 || c < 0) continue;
+        if (p >= t.rows || c >= t.rows) {
+            if (table && tid == 0) tell(status, GDN_DEV_BAD_SLOT);
+            continue;
+        }
+        const int len = __ldg(t.seq_lens + p);      // a parent is no child: nobody writes it
+        bool clash = p == c;
+        for (int q = tid; q < n; q += kCopyThreads) {
+            const int qp = __ldg(parents + q), qc = __ldg(children + q);
+            if (q != k && qp >= 0 && qc >= 0 && (qc == c || qp == c || qc == p)) clash = true;
+        }
+        clash = __syncthreads_or(clash);
+        if (clash || !length_ok(t, len)) {
+            if (table && tid == 0) tell(status, clash ? GDN_DEV_CONFLICT : GDN_DEV_BAD_LENGTH);
+            continue;
+        }
+        if (!table) {
+            copy_piece(ps, (int)((i - table_blocks) % ps.pieces), p, c);
+            continue;
+        }
+        const int old = *reinterpret_cast<const volatile int32_t *>(t.seq_lens + c);
+        __syncthreads();                            // read by all before it is written
+        const int want = pages_of(len, t.page_size);
+        const int had = length_ok(t, old) ? pages_of(old, t.page_size) : 0;
+        const int32_t *const from = t.block_table + p * t.table_stride;
+        int32_t *const to = t.block_table + c * t.table_stride;
+        for (int j = tid; j < max(had, want); j += kCopyThreads) {
+            if (!in_range(j, 1, t.width, status)) break;
+            const int give = j < had ? to[j] : 0, take = j < want ? __ldg(from + j) : -1;
+            if (j < had) {
+                if ((uint32_t)give < (uint32_t)t.num_pages)
+                    atomicSub(t.ref_count + give, 1);
+                else
+                    tell(status, GDN_DEV_BAD_PAGE);
+            }
+            if (j < want) {
+                if ((uint32_t)take < (uint32_t)t.num_pages)
+                    atomicAdd(t.ref_count + take, 1);
+                else
+                    tell(status, GDN_DEV_BAD_PAGE);
+            }
+            to[j] = take;
+        }
+        if (tid == 0) {
+            t.seq_lens[c] = len;
+            if (!length_ok(t, old)) tell(status, GDN_DEV_BAD_LENGTH);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ host
+int access_width(const gdn_pool &p)
+{
+    const uint64_t x = (uint64_t)(uintptr_t)p.data | (uint64_t)p.row_stride | (uint64_t)p.row_bytes;
+    return x % 16 == 0 ? 16 : (x % 4 == 0 ? 4 : (x % 2 == 0 ? 2 : 1));
+}
+
+// pools [first, first + kMaxPools) of the call
+Pools take_pools(const gdn_pool *pools, int n_pools, int first)
+{
+    Pools ps;
+    ps.n = ps.pieces = 0;
+    for (int i = first; i < n_pools && ps.n < kMaxPools; ++i) {
+        Pool &p = ps.p[ps.n++];
+        p.data = static_cast<unsigned char *>(pools[i].data);
+        p.stride = pools[i].row_stride;
+        p.bytes = pools[i].row_bytes;
+        p.first = ps.pieces;
+        p.width = access_width(pools[i]);
+        ps.pieces += (int)((p.bytes + kCopyBytes - 1) / kCopyBytes);
+    }
+    return ps;
+}
+
+unsigned copy_blocks(int64_t items)
+{
+    const int64_t most = 8 * (int64_t)sm_count();   // resident blocks of kCopyThreads
+    return (unsigned)(items < 1 ? 1 : (items < most ? items : most));
+}
+
+cudaError_t launch_copies(const gdn_page_table &t, const gdn_pool *pools, int n_pools,
+                          const int2 *pairs, const int *count, int64_t most_pairs,
+                          const int32_t *map, int32_t *status, cudaStream_t stream)
+{
+    for (int first = 0; first < n_pools || (first == 0 && map); first += kMaxPools) {
+        const Pools ps = take_pools(pools, n_pools, first);
+        int64_t items = most_pairs * ps.pieces;
+        const int32_t *const m = first == 0 ? map : nullptr;
+        if (m) {
+            const int64_t renames = (int64_t)t.rows * t.width / kCopyThreads + 1;
+            items = items > renames ? items : renames;
+        }
+        const cudaError_t e = launch_dependent(copy_pairs_kernel, dim3(copy_blocks(items)),
+                                               dim3(kCopyThreads), 0, stream, ps, pairs, count,
+                                               t.num_pages, t, m, status);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+uint64_t up16(uint64_t x) { return (x + 15) / 16 * 16; }
+
+}  // namespace gdn_pages
+
+uint64_t page_workspace_bytes(int32_t num_pages, int32_t n)
+{
+    using namespace gdn_pages;
+    if (n > 0)
+        return 16 + up16((uint64_t)n * sizeof(int2)) + (uint64_t)kCluster * n * sizeof(Row) +
+               up16((uint64_t)num_pages * 4);
+    return 16 + up16((uint64_t)num_pages * sizeof(int2)) + 2 * up16((uint64_t)num_pages * 4);
+}
+
+cudaError_t launch_page_resize(const gdn_page_table &t, const int32_t *row_list,
+                               const int32_t *new_lens, int32_t n, const gdn_pool *pools,
+                               int32_t n_pools, void *workspace, int32_t *dev_status,
+                               cudaStream_t stream)
+{
+    using namespace gdn_pages;
+    unsigned char *const w = static_cast<unsigned char *>(workspace);
+    ResizeWork ws;
+    ws.count = reinterpret_cast<int *>(w);
+    ws.pairs = reinterpret_cast<int2 *>(w + 16);
+    unsigned char *const r = w + 16 + up16((uint64_t)n * sizeof(int2));
+    ws.rows = reinterpret_cast<Row *>(r);
+    ws.free_list = reinterpret_cast<int *>(r + (uint64_t)kCluster * n * sizeof(Row));
+    resize_kernel<<<kCluster, kThreads, 0, stream>>>(t, row_list, new_lens, n, ws, dev_status);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return launch_copies(t, pools, n_pools, ws.pairs, ws.count, n, nullptr, dev_status, stream);
+}
+
+cudaError_t launch_page_compact(const gdn_page_table &t, int32_t *page_map, const gdn_pool *pools,
+                                int32_t n_pools, void *workspace, int32_t *dev_status,
+                                cudaStream_t stream)
+{
+    using namespace gdn_pages;
+    unsigned char *const w = static_cast<unsigned char *>(workspace);
+    CompactWork ws;
+    ws.count = reinterpret_cast<int *>(w);
+    ws.pairs = reinterpret_cast<int2 *>(w + 16);
+    unsigned char *const u = w + 16 + up16((uint64_t)t.num_pages * sizeof(int2));
+    ws.used = reinterpret_cast<int *>(u);
+    ws.open = reinterpret_cast<int *>(u + up16((uint64_t)t.num_pages * 4));
+    compact_kernel<<<kCluster, kThreads, 0, stream>>>(t, page_map, ws, dev_status);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return launch_copies(t, pools, n_pools, ws.pairs, ws.count, t.num_pages / 2, page_map,
+                         dev_status, stream);
+}
+
+cudaError_t launch_page_fork(const gdn_page_table &t, const int32_t *parents,
+                             const int32_t *children, int32_t n, const gdn_pool *pools,
+                             int32_t n_pools, int32_t *dev_status, cudaStream_t stream)
+{
+    using namespace gdn_pages;
+    for (int first = 0; first == 0 || first < n_pools; first += kMaxPools) {
+        const Pools ps = take_pools(pools, n_pools, first);
+        const int table_blocks = first == 0 ? n : 0;
+        const int64_t items = table_blocks + (int64_t)n * ps.pieces;
+        fork_kernel<<<copy_blocks(items), kCopyThreads, 0, stream>>>(ps, t, parents, children, n,
+                                                                     table_blocks, dev_status);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}

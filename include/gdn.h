@@ -2,11 +2,17 @@
  * gdn.h -- C ABI of libgdn: the Gated DeltaNet recurrence on NVIDIA B200
  * (sm_100a).
  *
- * Three entry points:
+ * The recurrence and its conv:
  *   gdn_prefill  chunked / sequential scan over ragged requests;
  *   gdn_decode   decode / MTP update of an fp32 slot-indexed state pool;
  *   gdn_conv1d   the causal depthwise conv1d that feeds q, k, v, with a
  *                slot-indexed pool of conv windows.
+ * The paged key-value cache of the softmax layers a hybrid model puts between them:
+ *   gdn_kv_append     new keys and values go to the pages of their positions;
+ *   gdn_paged_attn    a request's last tokens attend to its pages;
+ *   gdn_page_resize   rows of the page table grow, shrink and are freed;
+ *   gdn_page_fork     rows share another's pages and copy its recurrent state;
+ *   gdn_page_compact  the used pages move to the lowest numbers.
  *
  * Conventions shared by every call
  *   - Every tensor argument is a DEVICE pointer owned by the caller.  The
@@ -19,14 +25,17 @@
  *     host and never synchronises, so a call may be captured in a CUDA graph.
  *   - Inputs are never modified.  The only buffers written are `out`,
  *     `final_state` (prefill), `state_pool`, `out` (decode) and `out`,
- *     `conv_state` (conv1d), plus the optional `dev_status` word.
+ *     `conv_state` (conv1d), the cache, tables, pools, `out`, `lse` and
+ *     `page_map` that the cache's calls name, workspaces, and the optional
+ *     `dev_status` word.
  *   - Errors the host can see (null pointers, shapes, alignment, aliasing,
  *     unsupported sizes) are returned as a gdn_status before anything is
  *     launched.  Errors only the device can see (a slot index >= pool_size)
  *     skip the affected unit and OR a GDN_DEV_* bit into *dev_status when
  *     `dev_status` is non-NULL.  No kernel traps or asserts.
  *   - Layouts are dense, row-major, with the strides implied by the shapes
- *     below (decode's pool alone takes explicit strides).
+ *     below (decode's pool, the paged cache, the rows that go into it and the
+ *     queries that read it take explicit strides).
  */
 #ifndef GDN_H
 #define GDN_H
@@ -57,7 +66,8 @@ typedef enum {
 typedef enum {
     GDN_F32 = 0,   /* float32 activations */
     GDN_BF16 = 1,  /* bfloat16 activations */
-    GDN_F16 = 2    /* float16 activations (prefill, conv1d) */
+    GDN_F16 = 2,   /* float16 activations (prefill, conv1d, the paged cache) */
+    GDN_E4M3 = 3   /* 8-bit floats of 4 exponent and 3 mantissa bits (the paged cache only) */
 } gdn_dtype;
 
 /* flags */
@@ -73,7 +83,8 @@ enum {
     GDN_RULE_MASK = 3u << 3,
     GDN_GATE_QWEN = 1u << 5,            /* prefill: g <- -exp(a_log[h]) softplus(g + dt_bias[h]) */
     GDN_BETA_SIGMOID = 1u << 6,         /* prefill: beta <- sigmoid(beta) */
-    GDN_DECAY_PER_KEY = 1u << 8         /* prefill: g is [N, Hv, Dk], one decay per key dimension */
+    GDN_DECAY_PER_KEY = 1u << 8,        /* prefill: g is [N, Hv, Dk], one decay per key dimension */
+    GDN_ZERO_PADDING = 1u << 9          /* paged_attn: padding rows get zeros instead of nothing */
 };
 
 /* bits OR-ed into *dev_status by the kernels */
@@ -85,6 +96,10 @@ enum {
      * data-dependent shared-memory access is tested against its buffer first; one outside it
      * is skipped (a load reads zero) and this bit is set.  Ordinary builds never set it. */
     GDN_DEV_BOUNDS = 8,
+    GDN_DEV_BAD_PAGE = 16,    /* a page that a row's length needs is not in [0, num_pages) */
+    GDN_DEV_BAD_LENGTH = 32,  /* a length outside what a row of the page table holds */
+    GDN_DEV_CONFLICT = 64,    /* a row listed twice, or as a child and as a parent: left undone */
+    GDN_DEV_NO_PAGES = 128,   /* too few free pages: the rows that did not fit are left undone */
     /* Checked builds only, set by the CALLER in *dev_status before a gdn_decode or a
      * chunked gdn_prefill call: the persistent decode kernel, or the chunked prefill
      * kernel's first q/k stage, posts 16 bytes more than its copies deliver (the per-key
@@ -352,6 +367,198 @@ GDN_API gdn_status gdn_conv1d(const void *x, const void *weight, void *conv_stat
                               void *out, int32_t B, int64_t N, int32_t conv_dim,
                               int32_t kernel_size, int32_t max_slots, gdn_dtype dtype,
                               int32_t write_state, int32_t *dev_status, void *stream);
+
+/*
+ * The paged key-value cache
+ *
+ * A softmax layer keeps one key and one value vector for each token and head.  They lie in
+ * pages of `page_size` tokens; row s of the page table names the pages of request s in order,
+ * so that position j is at offset j % page_size of page block_table[s][j / page_size], and
+ * seq_lens[s] is how many positions the row holds.  Row s is the slot that the same request
+ * has in the state pool of gdn_decode and the window pool of gdn_conv1d, so that one number
+ * names a request in every layer.  ref_count[p] counts the rows that hold page p (and
+ * whatever else the caller keeps a page for); a page whose count is zero or less is free.
+ *
+ * One step of decoding: gdn_page_resize lengthens the rows by the step's tokens, then in each
+ * softmax layer gdn_kv_append writes the tokens' keys and values and gdn_paged_attn reads the
+ * cache.  A verified draft that was partly rejected is cut by another gdn_page_resize.
+ */
+
+/* The cache of one layer.  Read by the call on the host; keeps no reference afterwards. */
+typedef struct {
+    void *k, *v;             /* device: page p, token o, head h, dimension i at
+                                p*page_stride + o*token_stride + h*head_stride + i, the same
+                                strides for both (in elements, multiples of 16 bytes; that of a
+                                dimension of one does not matter) */
+    int64_t page_stride, token_stride, head_stride;
+    const float *k_scale, *v_scale;  /* [heads] float32 or NULL (ones): GDN_E4M3 only, what a
+                                        stored number is multiplied by to give its value */
+    const int32_t *block_table;      /* [rows, width], rows `table_stride` entries apart */
+    const int32_t *seq_lens;         /* [rows] */
+    int64_t table_stride;
+    int32_t rows, width;
+    int32_t num_pages, page_size;
+    int32_t heads, head_dim;
+    int32_t dtype;                   /* GDN_BF16, GDN_F16 or GDN_E4M3 */
+} gdn_paged_cache;
+
+/*
+ * gdn_kv_append -- write new tokens' keys and values to the pages of their positions.
+ *
+ * Request b of B has the tokens [s, e) = [row_offsets[b], row_offsets[b+1]) of k and v (clamped
+ * to [0, N]; e <= s is empty), or with row_offsets NULL the tokens [b*N/B, (b+1)*N/B).  They
+ * are the last e - s positions of row slots[b] of the cache, whose seq_lens entry counts them
+ * already: token s + i goes to position seq_lens[slot] - (e - s) + i.
+ *   16-bit cache   the values are stored as they are (k, v and the cache have one type);
+ *   GDN_E4M3       round(clamp(x / scale[h], -448, 448)) to the nearest of the type's numbers,
+ *                  ties to even; a NaN stays one.  The quotient is taken in float32.
+ *
+ * Arguments (N = tokens, B = requests, H = cache->heads, D = cache->head_dim):
+ *   k, v          token n, head h at n*token_stride + h*head_stride (elements), D dense
+ *   slots         [B] int32 or NULL (request b is row b); a negative slot is padding: its
+ *                 tokens are not written
+ *   row_offsets   [B+1] int32, or NULL (then N % B == 0)
+ *   dtype         of k and v: GDN_BF16 or GDN_F16
+ *   dev_status    GDN_DEV_BAD_SLOT: slot >= rows (the request is skipped);
+ *                 GDN_DEV_BAD_LENGTH: a token's position is negative or past the row's width;
+ *                 GDN_DEV_BAD_PAGE: its page is not one (such tokens are skipped).
+ * Requirements: D a multiple of 8 (GDN_E4M3: of 16) and at most 256; k, v and the cache
+ * 16-byte aligned with strides that are multiples of 16 bytes (8 elements for k and v); the
+ * strides of the cache keep its vectors apart.  Requests name distinct rows.  Nothing else
+ * of the cache is touched.
+ */
+GDN_API gdn_status gdn_kv_append(const void *k, const void *v, int64_t k_token_stride,
+                                 int64_t k_head_stride, int64_t v_token_stride,
+                                 int64_t v_head_stride, const gdn_paged_cache *cache,
+                                 const int32_t *slots, const int32_t *row_offsets, int32_t B,
+                                 int64_t N, gdn_dtype dtype, int32_t *dev_status, void *stream);
+
+/*
+ * gdn_paged_attn -- softmax attention of each request's last T tokens over its pages.
+ *
+ * Request b has row s = slots[b] of the cache, of length n = seq_lens[s]; its token t stands at
+ * position n - T + t and sees the positions j <= n - T + t, of them with window > 0 the last
+ * `window` only.  Query head h reads head floor(h * H / Hq) of the cache:
+ *     x_j = scale * q . k_j,   lse = log sum_j exp(x_j),   out = sum_j exp(x_j - lse) v_j
+ * in float32 (scores, maxima, sums and accumulators), with the probabilities rounded to the
+ * cache's 16-bit type (fp16 for GDN_E4M3) before they meet the values.  A token that sees
+ * nothing (n = 0, or fewer than T positions) gets out = 0 and lse = -inf; a position whose
+ * score is -inf has no weight.  Positions that a token does not see never reach its output,
+ * whatever they hold (infinities and NaN included).
+ *
+ * Arguments (B requests, H = cache->heads, D = cache->head_dim):
+ *   q      token t of request b, head h at (b*T + t)*q_token_stride + h*q_head_stride
+ *   slots  [B] int32 or NULL (request b is row b); a negative slot is padding: its rows of out
+ *          and lse keep the caller's values, or get 0 and -inf with GDN_ZERO_PADDING
+ *   dtype  of q and out: GDN_BF16 or GDN_F16, the cache's type or any of the two over GDN_E4M3
+ *   scale  applied as given (the Python binding maps None to 1/sqrt(D))
+ *   window 0: every position up to the token's own
+ *   out    [B, T, Hq, D] `dtype`;  lse [B, T, Hq] float32 or NULL
+ *   flags  GDN_ZERO_PADDING or 0
+ *   workspace  device memory of gdn_paged_attn_workspace_size(...) bytes, 16-byte aligned,
+ *          holds the parts of requests that several blocks share until they are joined; its
+ *          contents do not matter before or after (calls sharing one must be ordered)
+ *   dev_status GDN_DEV_BAD_SLOT: slot >= rows (treated as a row of length 0);
+ *          GDN_DEV_BAD_LENGTH: a length below 0 or above width * page_size (cut to it);
+ *          GDN_DEV_BAD_PAGE: a page that is not one (its positions are not seen).
+ * Requirements: 1 <= T <= 16; Hq % H == 0; D a multiple of 8 (GDN_E4M3: of 16), at most 256;
+ * page_size >= 1; q and out 4-byte aligned with even strides, the cache as for gdn_kv_append.
+ */
+GDN_API gdn_status gdn_paged_attn(const void *q, int64_t q_token_stride, int64_t q_head_stride,
+                                  const gdn_paged_cache *cache, const int32_t *slots, int32_t B,
+                                  int32_t T, int32_t Hq, gdn_dtype dtype, float scale,
+                                  int32_t window, void *out, float *lse, uint32_t flags,
+                                  void *workspace, uint64_t workspace_bytes,
+                                  int32_t *dev_status, void *stream);
+
+/* Workspace bytes gdn_paged_attn needs for these sizes on the current device (0 without one, or
+ * for sizes it does not take).  Host-only. */
+GDN_API uint64_t gdn_paged_attn_workspace_size(int32_t B, int32_t T, int32_t Hq, int32_t heads,
+                                               int32_t head_dim, gdn_dtype cache_dtype);
+
+/* The page table of the cache's rows and the counts of its pages, shared by all layers. */
+typedef struct {
+    int32_t *block_table;    /* [rows, width], rows `table_stride` entries apart; entries past
+                                a row's pages are -1 */
+    int32_t *ref_count;      /* [num_pages] */
+    int32_t *seq_lens;       /* [rows] */
+    int64_t table_stride;
+    int32_t rows, width;
+    int32_t num_pages, page_size;
+} gdn_page_table;
+
+/* An array of rows in device memory: row i is the row_bytes bytes at data + i * row_stride. */
+typedef struct {
+    void *data;
+    int64_t row_stride, row_bytes;   /* bytes; row_stride >= row_bytes */
+} gdn_pool;
+
+/*
+ * gdn_page_resize -- give listed rows of the page table new lengths.
+ *
+ * In this order:
+ *   1. a row that gets shorter gives back the pages past its new length: ref_count - 1, table
+ *      entry -1 (length 0 frees the row);
+ *   2. rows that get longer take the lowest-numbered free pages, in the order of the list, each
+ *      with ref_count 1.  Where the page that holds the last position is partly filled and has
+ *      ref_count > 1 (a fork shares it), the row takes one more page first, which replaces the
+ *      shared one (ref_count - 1) and gets its contents in every pool.  After the call no other
+ *      row holds the pages of the positions that a row gained.
+ * Where the free pages run out, that row and the ones after it that need a page are left as
+ * they were (GDN_DEV_NO_PAGES).  Pages that step 2 gives up are free from the next call on.
+ *
+ * Arguments: row_list, new_lens [n] int32 (a negative row is padding and is skipped);
+ * pools [n_pools], host memory: the arrays whose rows are pages (keys and values of each
+ * layer), num_pages rows each; workspace of gdn_page_workspace_size(...) bytes, 16-byte aligned.
+ * dev_status: GDN_DEV_BAD_SLOT (row >= rows), GDN_DEV_BAD_LENGTH (a length, old or new, outside
+ * [0, width * page_size]), GDN_DEV_CONFLICT (a row listed twice), GDN_DEV_BAD_PAGE (a shared
+ * last page that is not one): such rows are left as they were, in all places they are listed.
+ * A page past the new length that is not one is dropped from the table (GDN_DEV_BAD_PAGE).
+ */
+GDN_API gdn_status gdn_page_resize(const gdn_page_table *table, const int32_t *row_list,
+                                   const int32_t *new_lens, int32_t n, const gdn_pool *pools,
+                                   int32_t n_pools, void *workspace, uint64_t workspace_bytes,
+                                   int32_t *dev_status, void *stream);
+
+/*
+ * gdn_page_fork -- child rows become copies of parent rows, sharing their pages.
+ *
+ * For each pair: the pages that the child held are given back (ref_count - 1), the parent's are
+ * shared (ref_count + 1, same table entries), the child gets the parent's length, and in every
+ * pool row `child` becomes a copy of row `parent`.  The pools are the slot-indexed ones: the
+ * recurrent states and the conv windows.  Pages are not copied: the first of the holders to
+ * grow into a shared page gets its own (gdn_page_resize).
+ *
+ * Arguments: parents, children [n] int32 (a pair with a negative entry is padding);
+ * pools [n_pools], host memory, with table->rows rows each.  dev_status: GDN_DEV_BAD_SLOT (an
+ * entry >= rows), GDN_DEV_CONFLICT (pairs of which one's child is the other's child or parent,
+ * or a row that is its own parent), GDN_DEV_BAD_LENGTH (a parent's length outside [0, width *
+ * page_size]): such pairs are left undone.  A child whose own length is outside gives nothing
+ * back (GDN_DEV_BAD_LENGTH).  GDN_DEV_BAD_PAGE: a table entry that is not a page was copied or
+ * dropped without a count.  A parent may have any number of children.  Every pair is compared
+ * with every other, which for some thousands of pairs costs more than small copies do.
+ */
+GDN_API gdn_status gdn_page_fork(const gdn_page_table *table, const int32_t *parents,
+                                 const int32_t *children, int32_t n, const gdn_pool *pools,
+                                 int32_t n_pools, int32_t *dev_status, void *stream);
+
+/*
+ * gdn_page_compact -- move the used pages to the lowest numbers.
+ *
+ * With U pages in use (ref_count > 0), the k-th used page of number >= U moves to the k-th free
+ * page of number < U, both in ascending order, in every pool; counts and table entries follow.
+ * Afterwards pages [0, U) are used and the others free.  page_map [num_pages] int32, written:
+ * the new number of each used page, -1 for free ones (for holders of pages outside the table).
+ * Arguments otherwise as gdn_page_resize.  dev_status: GDN_DEV_BAD_LENGTH (that row's table
+ * entries are left as they were), GDN_DEV_BAD_PAGE (a table entry that is no used page, left).
+ */
+GDN_API gdn_status gdn_page_compact(const gdn_page_table *table, int32_t *page_map,
+                                    const gdn_pool *pools, int32_t n_pools, void *workspace,
+                                    uint64_t workspace_bytes, int32_t *dev_status, void *stream);
+
+/* Workspace bytes of gdn_page_resize with n listed rows, or of gdn_page_compact (n = 0), for
+ * tables of num_pages pages.  Host-only. */
+GDN_API uint64_t gdn_page_workspace_size(int32_t num_pages, int32_t n);
 
 /* 1 when gdn_prefill with these arguments runs a chunked tensor-core kernel,
  * 0 when it runs the per-token kernel (host-only query, no launch).  The chunked
