@@ -16,15 +16,20 @@
 //     keys and 16 KB of values.  All tiles of all units in a row are dealt to the resident
 //     blocks (two an SM) in equal runs, found on the device from the lengths: one long request
 //     and many short ones fill the GPU alike, and the host reads nothing.
-//   - A block streams its run through three stages of shared memory with 16-byte asynchronous
-//     copies, rows of a tile looked up in the page table one tile ahead; tokens that no row sees
-//     are zero-filled, never read.
+//   - In a block up to four warps walk the run: they look the tile's tokens up in the page table
+//     and fetch their pages with TMA (boxes of as many tokens as a power of two that divides the
+//     page size allows, 128-byte swizzle) into one of three stages of shared memory.
 //   - Four warps share a tile: WR over blocks of 16 rows, the others over the tokens (each with
 //     its own m, l, O, joined in shared memory at the end of the unit), and for 256-wide heads
-//     two over the halves of the values.
+//     two over the halves of the values.  They wait for a stage each for itself; no barrier of
+//     the block is in the loop.
 //   - A unit that lies in one block is finished there.  Parts of the others go to the workspace
 //     and a second kernel joins them in the order of the tokens: no atomics, the same result in
 //     every run.
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <type_traits>
 #include <cuda_runtime.h>
 
 #include "cache.cuh"
@@ -37,12 +42,15 @@ using gdn::in_smem;
 using sm100::ex2_approx;
 using sm100::smem_u32;
 
-constexpr int kThreads = 128;
+constexpr int kConsumers = 128;     // threads that compute: four warps
+constexpr int kThreads = 256;       // and up to four that fetch: 128 registers a thread at launch,
+constexpr int kFetchRegs = 56;      // then 56 and 200
+constexpr int kComputeRegs = 200;
+static_assert(kFetchRegs + kComputeRegs == 2 * 128, "the block's registers, two blocks an SM");
 constexpr int kHalfStage = 16384;   // bytes of keys (or values) in a stage
 constexpr int kStages = 3;
-constexpr int kRing = 4;            // tile descriptors alive at once
 constexpr int kMergeBytes = 8192;
-constexpr int kRowsWindow = 64;     // rows of the batch whose lengths are at hand
+constexpr int kAlign = 1024;        // of a stage: where the swizzle's pattern begins
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -52,14 +60,23 @@ template <int KIND, int DP, int WR>
 struct Cfg {
     static constexpr int ESZ = KIND == kE4M3 ? 1 : 2;
     static constexpr int RB = DP * ESZ;              // bytes of a token's row in a stage
-    static constexpr int CPR = RB / 16;              // 16-byte pieces of it
+    static constexpr int IB = RB < 128 ? RB : 128;   // bytes of a row in a box
+    static constexpr int HB = RB / IB;               // boxes side by side
     static constexpr int TILE = kHalfStage / RB;     // tokens a tile
     static constexpr int WD = DP == 256 ? 2 : 1;     // warps over the values' dimensions
     static constexpr int WT = 4 / (WR * WD);         // warps over tokens
-    static constexpr int NS = TILE / 16 / WT;        // 16-token steps of a warp in a tile
+    // Warps that fetch a tile, a share of its tokens each: looking 256 tokens up takes one warp
+    // longer than the memory takes for them.
+    static constexpr int FETCH = TILE / 32 < 4 ? TILE / 32 : 4;
+    static constexpr int FW = TILE / 32 / FETCH;     // 32 tokens each of a warp's share
+    // tokens a warp takes at a time: two blocks of 16, twice the independent products, where it
+    // has them and the registers hold them
+    static constexpr int STEP = ESZ == 1 || DP == 64 ? 32 : 16;
+    static constexpr int NS = TILE / WT / STEP;      // such steps of a warp in a tile
+    static constexpr int NX = STEP / 8;              // blocks of 8 columns of scores
     static constexpr int DW = DP / WD;               // dimensions a warp accumulates
     static constexpr int RMAX = 16 * WR;             // rows of a unit
-    static constexpr int SMEM = kStages * 2 * kHalfStage + kMergeBytes + 2 * TILE * 8;
+    static constexpr int SMEM = kStages * 2 * kHalfStage + kMergeBytes + kAlign;
     static_assert(WT >= 1 && NS >= 1, "four warps");
 };
 
@@ -103,35 +120,56 @@ __device__ __forceinline__ int first_seen(const GdnAttnArgs &a, int len)
     return a.window > 0 ? max(0, (int)max((int64_t)len - a.T - a.window + 1, (int64_t)0)) : 0;
 }
 
-template <int TILE>
-__device__ __forceinline__ int tiles_of(const GdnAttnArgs &a, int len)
+// first position of the first tile: boxes do not cross pages
+__device__ __forceinline__ int first_tile(const GdnAttnArgs &a, int len, int box)
 {
-    const int lo = first_seen(a, len);
-    return len > lo ? (len - lo + TILE - 1) / TILE : 0;
+    return first_seen(a, len) & ~(box - 1);
 }
 
-__device__ __forceinline__ int64_t block_sum(int64_t x, int64_t *s)
+template <int TILE>
+__device__ __forceinline__ int tiles_of(const GdnAttnArgs &a, int len, int box)
 {
+    return len > first_seen(a, len) ? (len - first_tile(a, len, box) + TILE - 1) / TILE : 0;
+}
+
+// inclusive prefix sum over the block's threads; *total is the same in all
+__device__ __forceinline__ int64_t block_scan(int64_t x, int64_t *s, int64_t *total)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = x;
+    for (int d = 1; d < 32; d <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+        if (lane >= d) x += y;
+    }
+    if (lane == 31) s[warp] = x;
     __syncthreads();
-    x = s[0] + s[1] + s[2] + s[3];
+    int64_t all = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) x += s[w];
+        all += s[w];
+    }
+    *total = all;
     __syncthreads();
     return x;
 }
 
-// rows and dimensions of a finished or partial result
-template <int KIND, int DP, int WR>
-struct Where {
-    using C = Cfg<KIND, DP, WR>;
-    // first of the pair of dimensions held in o[n][e], o[n][e + 1] (16 bits), or of the four in
-    // o[n][e], o[n + 1][e], o[n][e + 1], o[n + 1][e + 1] (e4m3, n even)
-    static __device__ __forceinline__ int dim(int n, int tq)
-    {
-        return KIND == kE4M3 ? n * 8 + 4 * tq : n * 8 + 2 * tq;
+// Wait for a phase of a barrier, about a second at most: then GDN_DEV_TIMEOUT is set, and from
+// there on no wait of the block waits (its outputs are invalid), so that all its warps reach the
+// end.
+__device__ __forceinline__ void wait_phase(uint32_t bar, uint32_t parity, volatile int *abort, int32_t *status)
+{
+    if (sm100::mbar_try_wait(bar, parity)) return;
+    const long long start = clock64();
+    while (!sm100::mbar_try_wait(bar, parity)) {
+        if (*abort) return;
+        if (clock64() - start > (1ll << 31)) {
+            *abort = 1;
+            if (status) atomicOr(status, GDN_DEV_TIMEOUT);
+            return;
+        }
     }
-};
+}
 
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack16(float lo, float hi)
@@ -147,60 +185,194 @@ __device__ __forceinline__ uint32_t pack_out(bool bf16, float lo, float hi)
     return bf16 ? gdn::pack_bf16x2(lo, hi) : pack_f16x2(lo, hi);
 }
 
-// 16-byte piece c of token row r of a stage: keys and values of 16 bits and values of 8 are read
-// by ldmatrix (eight rows, one piece), keys of 8 bits four pieces of two rows at a time
-template <int RB, bool QUADS>
+// byte of 16-byte piece c of token r in the keys or values of a stage
+template <class C>
 __device__ __forceinline__ int piece(int r, int c)
 {
-    if constexpr (QUADS) return RB == 64 ? c : c ^ ((r & 1) << 2);
-    return RB == 64 ? c ^ ((r >> 1) & 3) : c ^ (r & 7);
+    if constexpr (C::IB == 64) return r * 64 + (c ^ ((r >> 1) & 3)) * 16;
+    return (c >> 3) * (C::TILE * 128) + r * 128 + ((c & 7) ^ (r & 7)) * 16;
+}
+
+// Token (of the step's) that column `col` of the n-th block of 8 stands for.  In 8 bits the order
+// is such that the four tokens of a byte-wise transposed load are the two pairs that a thread's
+// probabilities of two blocks make, that the two tokens whose keys eight threads read together
+// lie in different banks, and so do the eight whose values are loaded together.
+template <class C>
+__device__ __forceinline__ int token_of(int n, int col)
+{
+    if constexpr (C::ESZ == 2) return n * 8 + col;
+    const int i = n & 1, j = col & 1, t = col >> 1;
+    return 16 * (n >> 1) + (t >> 1) * 8 + (t & 1) * 2 + (C::RB == 64 ? j + 4 * i : 4 * j + i);
 }
 
 template <int KIND, int DP, int WR>
 __global__ void __launch_bounds__(kThreads, 2)
-paged_attn_kernel(const GdnAttnArgs a, const int RT, Split *const splits, const int n_splits,
-                  float2 *const part_ml, float *const part_o)
+paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                  const __grid_constant__ GdnAttnArgs a, const int box, const int RT, Split *const splits,
+                  const int n_splits, float2 *const part_ml, float *const part_o)
 {
     using C = Cfg<KIND, DP, WR>;
-    constexpr int TILE = C::TILE, RB = C::RB, CPR = C::CPR;
+    constexpr int TILE = C::TILE;
     constexpr bool BF16 = KIND == kBF16;
-    extern __shared__ __align__(128) unsigned char smem[];
-    unsigned char *const s_stage = smem;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *const smem = smem_raw + (kAlign - (smem_u32(smem_raw) & (kAlign - 1))) % kAlign;
     float *const s_merge = reinterpret_cast<float *>(smem + kStages * 2 * kHalfStage);
-    int64_t *const s_off = reinterpret_cast<int64_t *>(smem + kStages * 2 * kHalfStage + kMergeBytes);
-    __shared__ int64_t s_sum[4];
+    __shared__ __align__(8) uint64_t s_full[kStages], s_empty[kStages];
+    __shared__ int64_t s_sum[kThreads / 32];
     __shared__ int64_t s_found[2];
-    __shared__ Desc s_desc[kRing];
-    __shared__ uint32_t s_valid[kRing][TILE / 32];
-    __shared__ RowInfo s_rows[kRowsWindow];
+    __shared__ Desc s_desc[kStages];
+    __shared__ uint32_t s_valid[kStages][TILE / 32];
     __shared__ float4 s_stat[2][32];
+    __shared__ volatile int s_abort;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int tq = lane & 3, lr = lane >> 2;
-    const int wr = warp % WR, wd = (warp / WR) % C::WD, wt = warp / (WR * C::WD);
     const int c = blockIdx.x, G = gridDim.x;
     const gdn_paged_cache &kv = a.cache;
     const int H = kv.heads, D = kv.head_dim, group = a.Hq / H, rows_all = a.T * group;
     const int U = H * RT;                              // units of a request
     const bool by_unit = (int64_t)a.B * U <= n_splits; // one Split a unit, else one a block
+    const uint32_t full0 = smem_u32(s_full), empty0 = smem_u32(s_empty);
 
     launch_dependents();
+    if (tid == 0) {
+        s_abort = 0;
+        for (int s = 0; s < kStages; ++s) {
+            sm100::mbar_init(full0 + 8 * s, C::FETCH);
+            sm100::mbar_init(empty0 + 8 * s, kConsumers / 32);
+        }
+        sm100::fence_mbar_init();
+        sm100::prefetch_tmap(&kmap);
+        sm100::prefetch_tmap(&vmap);
+        if (!by_unit && in_range(c, 1, n_splits, a.dev_status)) splits[c].c1 = -1;
+    }
 
     // ---- this block's run of tiles
-    int64_t mine = 0;
-    for (int b = tid; b < a.B; b += kThreads) mine += tiles_of<TILE>(a, row_info(a, b, c == 0).len);
-    const int64_t W = block_sum(mine, s_sum) * U;
+    int64_t S = 0;      // tiles of the batch, a unit of each request
+    const int nt0 = tid < a.B ? tiles_of<TILE>(a, row_info(a, tid, c == 0).len, box) : 0;
+    {
+        int64_t mine = nt0;
+        for (int b = tid + kThreads; b < a.B; b += kThreads)
+            mine += tiles_of<TILE>(a, row_info(a, b, c == 0).len, box);
+        block_scan(mine, s_sum, &S);
+    }
+    const int64_t W = S * U;
     const int64_t Ge = W < G ? W : G;
     const int64_t t0 = c < Ge ? c * W / Ge : 0, t1 = c < Ge ? (c + 1) * W / Ge : 0;
     const int n_tiles = (int)(t1 - t0);
-    if (!by_unit && tid == 0 && in_range(c, 1, n_splits, a.dev_status)) splits[c].c1 = -1;
 
+    // the request, unit and tile where it begins
+    if (n_tiles > 0) {
+        int64_t before = 0;
+        for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+            const int b = b0 + tid;
+            const int nt = b0 == 0 ? nt0 : (b < a.B ? tiles_of<TILE>(a, row_info(a, b, false).len, box) : 0);
+            int64_t all;
+            const int64_t incl = before + block_scan(nt, s_sum, &all);
+            if (nt > 0 && t0 >= (incl - nt) * U && t0 < incl * U) {
+                s_found[0] = b;
+                s_found[1] = t0 - (incl - nt) * U;
+            }
+            before += all;
+            if (t0 < before * U) break;
+        }
+    }
+    __syncthreads();
+
+    if (warp >= kConsumers / 32) {
+        // ================================================================ the warps that fetch
+        registers_down<kFetchRegs>();
+        const int fw = warp - kConsumers / 32;
+        if (n_tiles == 0 || fw >= C::FETCH) return;
+        int cb = (int)s_found[0], win = cb;     // request; lane i knows about request win + i
+        RowInfo mine = cb + lane < a.B ? row_info(a, cb + lane, false) : RowInfo{-1, 0};
+        int len = __shfl_sync(0xffffffffu, mine.len, 0), slot = __shfl_sync(0xffffffffu, mine.slot, 0);
+        int cnt = tiles_of<TILE>(a, len, box);
+        int cu = (int)(s_found[1] / cnt), ct = (int)(s_found[1] - (int64_t)cu * cnt);
+        for (int i = 0; i < n_tiles; ++i) {
+            const int st = i % kStages;
+            const int base = first_tile(a, len, box) + ct * TILE, lo = first_seen(a, len);
+            const int h = cu / RT;
+            // a lane looks up a token of each 32
+            const int32_t *const row = kv.block_table + (int64_t)slot * kv.table_stride;
+            const int first = base + fw * C::FW * 32 + lane;
+            int page[C::FW];
+#pragma unroll
+            for (int w = 0; w < C::FW; ++w) {
+                const int j = first + w * 32;
+                const int pg = (int)((uint32_t)j / (uint32_t)kv.page_size);
+                page[w] = j < len && in_range(pg, 1, kv.width, a.dev_status) ? __ldg(row + pg) : -1;
+            }
+            if (i >= kStages) wait_phase(empty0 + 8 * st, ((i / kStages) & 1) ^ 1, &s_abort, a.dev_status);
+            int boxes = 0;
+#pragma unroll
+            for (int w = 0; w < C::FW; ++w) {
+                const int j = first + w * 32;
+                const bool ok = (uint32_t)page[w] < (uint32_t)kv.num_pages;
+                if (j < len && j >= lo && !ok && a.dev_status) atomicOr(a.dev_status, GDN_DEV_BAD_PAGE);
+                const uint32_t seen = __ballot_sync(0xffffffffu, ok && j >= lo);
+                if (lane == 0) s_valid[st][fw * C::FW + w] = seen;
+                if (!ok || ((j - base) & (box - 1)) != 0) page[w] = -1;    // not first of a box
+                boxes += __popc(__ballot_sync(0xffffffffu, page[w] >= 0));
+            }
+            if (lane == 0) {
+                if (fw == 0) {
+                    Desc d;
+                    d.b = cb; d.u = cu; d.base = base; d.len = len; d.tile = ct; d.nt = cnt;
+                    s_desc[st] = d;
+                }
+                const uint32_t more = i == 0 && c == 0 && fw == 0 && gdn::test_stall_requested(a.dev_status) ? 16 : 0;
+                sm100::mbar_arrive_expect_tx(full0 + 8 * st, (uint32_t)(boxes * box * C::RB * 2) + more);
+            }
+            __syncwarp();
+            const uint32_t ks = smem_u32(smem + st * 2 * kHalfStage), vs = ks + kHalfStage;
+#pragma unroll
+            for (int w = 0; w < C::FW; ++w)
+                if (page[w] >= 0) {
+                    const int j = first + w * 32;
+                    const uint32_t to = (j - base) * C::IB;
+                    const int at = (int)((uint32_t)j % (uint32_t)kv.page_size);
+#pragma unroll
+                    for (int k = 0; k < C::HB; ++k) {
+                        tma_load_4d(ks + k * TILE * 128 + to, &kmap, full0 + 8 * st, k * 128 / C::ESZ, at, h, page[w]);
+                        tma_load_4d(vs + k * TILE * 128 + to, &vmap, full0 + 8 * st, k * 128 / C::ESZ, at, h, page[w]);
+                    }
+                }
+            // the next tile of the run (past the last one the cursor may stand anywhere)
+            if (++ct == cnt) {
+                ct = 0;
+                if (++cu == U) {
+                    cu = 0;
+                    do {
+                        if (++cb >= a.B) break;
+                        if (cb - win >= 32) {
+                            win = cb;
+                            mine = cb + lane < a.B ? row_info(a, cb + lane, false) : RowInfo{-1, 0};
+                        }
+                        len = __shfl_sync(0xffffffffu, mine.len, cb - win);
+                        slot = __shfl_sync(0xffffffffu, mine.slot, cb - win);
+                        cnt = tiles_of<TILE>(a, len, box);
+                    } while (cnt == 0);
+                }
+            }
+        }
+        if (s_abort) {      // no copy may land after the block is gone: a short wait for each stage
+            const long long start = clock64();
+            for (int i = n_tiles > kStages ? n_tiles - kStages : 0; i < n_tiles; ++i)
+                while (!sm100::mbar_try_wait(full0 + 8 * (i % kStages), (i / kStages) & 1) &&
+                       clock64() - start < (1ll << 26)) {
+                }
+        }
+        return;
+    }
+
+    // ==================================================================== the warps that compute
+    registers_up<kComputeRegs>();
     // requests with nothing to see: zeros for a row of the cache, nothing (or zeros) for padding
     for (int b = c; b < a.B; b += G) {
         const RowInfo ri = row_info(a, b, false);
-        if (tiles_of<TILE>(a, ri.len) > 0) continue;
+        if (tiles_of<TILE>(a, ri.len, box) > 0) continue;
         if (by_unit)
-            for (int u = tid; u < U; u += kThreads)
+            for (int u = tid; u < U; u += kConsumers)
                 if (in_range((int64_t)b * U + u, 1, n_splits, a.dev_status))
                     splits[(int64_t)b * U + u].c1 = -1;
         if (ri.slot < 0 && !a.zero_padding) continue;
@@ -208,178 +380,34 @@ paged_attn_kernel(const GdnAttnArgs a, const int RT, Split *const splits, const 
         const int64_t total = (int64_t)a.B * rows;
         uint32_t *const o = static_cast<uint32_t *>(a.out) + b * words;
         if (in_range(b * words, words, total * D / 2, a.dev_status))
-            for (int64_t i = tid; i < words; i += kThreads) o[i] = 0u;
+            for (int64_t i = tid; i < words; i += kConsumers) o[i] = 0u;
         if (a.lse && in_range(b * rows, rows, total, a.dev_status))
-            for (int64_t i = tid; i < rows; i += kThreads) a.lse[b * rows + i] = -INFINITY;
-    }
-    if (n_tiles == 0) return;
-
-    // the request, unit and tile where it begins
-    {
-        int64_t before = 0;
-        for (int b0 = 0; b0 < a.B; b0 += kThreads) {
-            const int b = b0 + tid;
-            const int nt = b < a.B ? tiles_of<TILE>(a, row_info(a, b, false).len) : 0;
-            int64_t incl = nt;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int64_t y = __shfl_up_sync(0xffffffffu, incl, d);
-                if (lane >= d) incl += y;
-            }
-            if (lane == 31) s_sum[warp] = incl;
-            __syncthreads();
-            int64_t all = 0;
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                if (w < warp) incl += s_sum[w];
-                all += s_sum[w];
-            }
-            incl += before;
-            if (nt > 0 && t0 >= (incl - nt) * U && t0 < incl * U) {
-                s_found[0] = b;
-                s_found[1] = t0 - (incl - nt) * U;
-            }
-            before += all;
-            __syncthreads();
-            if (t0 < before * U) break;
-        }
+            for (int64_t i = tid; i < rows; i += kConsumers) a.lse[b * rows + i] = -INFINITY;
     }
 
-    // cursor over the run (the same in every thread): where the next tile to prepare is
-    int cb = (int)s_found[0], win = cb;
-    auto fill_window = [&]() {
-        __syncthreads();
-        win = cb;
-        if (tid < kRowsWindow && win + tid < a.B) s_rows[tid] = row_info(a, win + tid, false);
-        __syncthreads();
-    };
-    fill_window();
-    RowInfo cr = s_rows[0];
-    int cnt = tiles_of<TILE>(a, cr.len);
-    int cu = (int)(s_found[1] / cnt), ct = (int)(s_found[1] - (int64_t)cu * cnt);
-    auto advance = [&]() {
-        if (++ct < cnt) return;
-        ct = 0;
-        if (++cu < U) return;
-        cu = 0;
-        do {
-            if (++cb >= a.B) return;  // past the last tile (never prepared)
-            if (cb - win >= kRowsWindow) fill_window();
-            cr = s_rows[cb - win];
-            cnt = tiles_of<TILE>(a, cr.len);
-        } while (cnt == 0);
-    };
-
-    // ---- a tile's rows: page lookups, then (a step later) its copies
-    constexpr int LPT = (TILE + kThreads - 1) / kThreads;   // lookups a thread
-    const int64_t cache_bytes = ((int64_t)(kv.num_pages - 1) * kv.page_stride +
-                                 (int64_t)(kv.page_size - 1) * kv.token_stride +
-                                 (int64_t)(H - 1) * kv.head_stride + D) * C::ESZ;
-    int64_t look[LPT];
-    auto lookup = [&]() {     // byte offset of each of this thread's token rows, or -1
-        const int base = first_seen(a, cr.len) + ct * TILE;
-        const int h = cu / RT;
-        const int32_t *const row = kv.block_table + (int64_t)cr.slot * kv.table_stride;
-#pragma unroll
-        for (int i = 0; i < LPT; ++i) {
-            const int j = base + tid + i * kThreads;
-            look[i] = -1;
-            if (tid + i * kThreads < TILE && j < cr.len) {
-                const int pg = (int)((uint32_t)j / (uint32_t)kv.page_size);
-                const int id = in_range(pg, 1, kv.width, a.dev_status) ? __ldg(row + pg) : -1;
-                if ((uint32_t)id < (uint32_t)kv.num_pages)
-                    look[i] = (id * kv.page_stride + (j - pg * kv.page_size) * kv.token_stride +
-                               h * kv.head_stride) * C::ESZ;
-                else if (a.dev_status)
-                    atomicOr(a.dev_status, GDN_DEV_BAD_PAGE);
-            }
-        }
-    };
-    auto note = [&](int n, const Desc &d) {   // write down tile n of the run
-#pragma unroll
-        for (int i = 0; i < LPT; ++i) {
-            const int r = tid + i * kThreads;
-            if (r < TILE) {      // whole warps: TILE is a multiple of 32
-                s_off[(n & 1) * TILE + r] = look[i];
-                const uint32_t ok = __ballot_sync(0xffffffffu, look[i] >= 0);
-                if (lane == 0) s_valid[n % kRing][r >> 5] = ok;
-            }
-        }
-        if (tid == 0) s_desc[n % kRing] = d;
-    };
-    auto here = [&]() {
-        Desc d;
-        d.b = cb; d.u = cu; d.base = first_seen(a, cr.len) + ct * TILE; d.len = cr.len;
-        d.tile = ct; d.nt = cnt;
-        return d;
-    };
-    const unsigned char *const kp = static_cast<const unsigned char *>(kv.k);
-    const unsigned char *const vp = static_cast<const unsigned char *>(kv.v);
-    auto issue = [&](int n) {
-        unsigned char *const st = s_stage + (n % kStages) * 2 * kHalfStage;
-        const uint32_t ks = smem_u32(st), vs = ks + kHalfStage;
-        const int ch = tid % CPR;
-        const bool has = ch * 16 < D * C::ESZ;
-#pragma unroll
-        for (int i = 0; i < kHalfStage / 16 / kThreads; ++i) {
-            const int r = tid / CPR + i * (kThreads / CPR);
-            const int64_t off = s_off[(n & 1) * TILE + r];
-            const bool ok = off >= 0 && has && in_range(off + ch * 16, 16, cache_bytes, a.dev_status);
-            const int64_t src = ok ? off + ch * 16 : 0;
-            const uint32_t bytes = ok ? 16u : 0u;
-            cp_async16(ks + r * RB + piece<RB, KIND == kE4M3>(r, ch) * 16, kp + src, bytes);
-            cp_async16(vs + r * RB + piece<RB, false>(r, ch) * 16, vp + src, bytes);
-        }
-    };
-
-    lookup();
-    note(0, here());
-    if (n_tiles > 1) {
-        advance();
-        lookup();
-        note(1, here());
-    }
-    __syncthreads();
-    issue(0);
-    cp_async_commit();
-    if (n_tiles > 1) issue(1);
-    cp_async_commit();
-    if (n_tiles > 2) {
-        __syncthreads();
-        advance();
-        lookup();
-        note(2, here());
-    }
-
+    const int tq = lane & 3, lr = lane >> 2;
+    const int wr = warp % WR, wd = (warp / WR) % C::WD, wt = warp / (WR * C::WD);
     // ---- the run
-    float m[2], l[2], o[C::DW / 8][4];      // rows lr and lr + 8 of the warp's 16
+    constexpr int E = 2, NX = C::NX;
+    float m[E], l[E], o[C::DW / 8][4];      // rows lr (and lr + 8) of the warp's
     uint32_t qf[DP / 16][4];
-    float xs[2];                            // what a raw score is multiplied by
-    int hi[2], lo[2];                       // a row sees lo < j <= hi
+    float xs[E];                            // what a raw score is multiplied by
+    int hi[E], lo[E];                       // a row sees lo < j <= hi
     int seg_tile = 0;                       // where the unit's part in this block began
 #pragma unroll 1
     for (int i = 0; i < n_tiles; ++i) {
-        cp_async_wait<kStages - 2>();
-        __syncthreads();
-        if (i + 2 < n_tiles) issue(i + 2);
-        cp_async_commit();
-        const bool more = i + 3 < n_tiles;
-        Desc next;
-        if (more) {
-            advance();
-            lookup();
-            next = here();
-        }
-        const Desc d = s_desc[i % kRing];
+        const int st = i % kStages;
+        wait_phase(full0 + 8 * st, (i / kStages) & 1, &s_abort, a.dev_status);
+        const Desc d = s_desc[st];
         const int h = d.u / RT, rt = d.u - h * RT;
 
         if (i == 0 || d.tile == 0) {        // a unit begins: its query rows
             seg_tile = d.tile;
             const float x2 = a.scale * kLog2e * (KIND == kE4M3 && kv.k_scale ? __ldg(kv.k_scale + h) : 1.f);
-            const uint32_t *qr[2];
-            bool has[2];
+            const uint32_t *qr[E];
+            bool has[E];
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
+            for (int e = 0; e < E; ++e) {
                 m[e] = -INFINITY;
                 l[e] = 0.f;
                 xs[e] = x2;
@@ -410,27 +438,25 @@ paged_attn_kernel(const GdnAttnArgs a, const int RT, Split *const splits, const 
                 // element to [2^7, 2^8): a bf16 or fp16 number down to 2^-22 of it is kept
                 // exactly, smaller ones to 2^-33 of it.  The order of the dimensions is that of
                 // the keys' 16-byte pieces: thread tq of a quad has 16 of each 64 in a row.
+                auto value = [&](uint32_t x, int half) {
+                    const uint16_t v = (uint16_t)(half ? x >> 16 : x & 0xffffu);
+                    return a.q_bf16 ? __uint_as_float((uint32_t)v << 16) : __half2float(__ushort_as_half(v));
+                };
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    uint32_t w[DP / 64][8];
+                    auto pair = [&](int s, int k) {
+                        const int dd = s * 64 + tq * 16 + 2 * k;
+                        return has[e] && dd < D ? __ldg(qr[e] + dd / 2) : 0u;
+                    };
+                    // two passes over the row, so that it need not be held twice
                     float top = 0.f;
 #pragma unroll
                     for (int s = 0; s < DP / 64; ++s)
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
-                            const int dd = s * 64 + tq * 16 + 2 * k;
-                            w[s][k] = has[e] && dd < D ? __ldg(qr[e] + dd / 2) : 0u;
+                            const uint32_t w = pair(s, k);
+                            top = fmaxf(top, fmaxf(fabsf(value(w, 0)), fabsf(value(w, 1))));
                         }
-                    auto value = [&](uint32_t x, int half) {
-                        const uint16_t v = (uint16_t)(half ? x >> 16 : x & 0xffffu);
-                        return a.q_bf16 ? __uint_as_float((uint32_t)v << 16)
-                                        : __half2float(__ushort_as_half(v));
-                    };
-#pragma unroll
-                    for (int s = 0; s < DP / 64; ++s)
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            top = fmaxf(top, fmaxf(fabsf(value(w[s][k], 0)), fabsf(value(w[s][k], 1))));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
                     const int ex = min(max((int)(__float_as_uint(top) >> 23), 8), 254);
@@ -439,145 +465,176 @@ paged_attn_kernel(const GdnAttnArgs a, const int RT, Split *const splits, const 
 #pragma unroll
                     for (int s = 0; s < DP / 64; ++s)
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            qf[s * 4 + k / 2][e + 2 * (k & 1)] =
-                                pack_f16x2(value(w[s][k], 0) * up, value(w[s][k], 1) * up);
+                        for (int k = 0; k < 8; ++k) {
+                            const uint32_t w = pair(s, k);
+                            qf[s * 4 + k / 2][e + 2 * (k & 1)] = pack_f16x2(value(w, 0) * up, value(w, 1) * up);
+                        }
                 }
             }
         }
 
-        const uint32_t ks = smem_u32(s_stage + (i % kStages) * 2 * kHalfStage), vs = ks + kHalfStage;
+        const uint32_t ks = smem_u32(smem + st * 2 * kHalfStage), vs = ks + kHalfStage;
         const int see_all = d.len - a.T;                                     // j <= this: causally seen by all rows
         const int64_t see_from = a.window > 0 ? (int64_t)d.len - a.window : 0;   // j >= this: in every window
 #pragma unroll 1
         for (int s = 0; s < C::NS; ++s) {
-            const int tok = (s * C::WT + wt) * 16;
-            const uint32_t ok = (s_valid[i % kRing][tok >> 5] >> (tok & 16)) & 0xffffu;
+            const int tok = (s * C::WT + wt) * C::STEP;
+            constexpr uint32_t kAll = C::STEP == 32 ? 0xffffffffu : 0xffffu;
+            const uint32_t ok = (s_valid[st][tok >> 5] >> (tok & 31)) & kAll;
             if (ok == 0) continue;
             const int j0 = d.base + tok;
-            const bool ragged = j0 + 15 > see_all || j0 < see_from;   // rows may see different tokens
+            const bool ragged = j0 + C::STEP - 1 > see_all || j0 < see_from;    // rows may see different tokens
 
-            // scores of 16 rows x 16 tokens
-            float x[2][4] = {};
+            // scores of the rows and STEP tokens
+            float x[NX][4] = {};
             if constexpr (KIND != kE4M3) {
                 const int r = tok + (lane & 7) + ((lane >> 4) << 3);
-                const uint32_t row = ks + r * RB;
 #pragma unroll
-                for (int k = 0; k < DP / 16; ++k) {
-                    uint32_t b[4];
-                    ldmatrix_x4(b, row + piece<RB, false>(r, 2 * k + ((lane >> 3) & 1)) * 16);
-                    mma_16816<BF16>(x[0], qf[k][0], qf[k][1], qf[k][2], qf[k][3], b[0], b[1]);
-                    mma_16816<BF16>(x[1], qf[k][0], qf[k][1], qf[k][2], qf[k][3], b[2], b[3]);
-                }
+                for (int k = 0; k < DP / 16; ++k)
+#pragma unroll
+                    for (int u = 0; u < NX / 2; ++u) {
+                        uint32_t b[4];
+                        ldmatrix_x4(b, ks + piece<C>(r + 16 * u, 2 * k + ((lane >> 3) & 1)));
+                        mma_16816<BF16>(x[2 * u], qf[k][0], qf[k][1], qf[k][2], qf[k][3], b[0], b[1]);
+                        mma_16816<BF16>(x[2 * u + 1], qf[k][0], qf[k][1], qf[k][2], qf[k][3], b[2], b[3]);
+                    }
             } else {
 #pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    const int r = tok + n * 8 + lr;
+                for (int q4 = 0; q4 < DP / 64; ++q4) {
+                    uint32_t w[NX][4];
 #pragma unroll
-                    for (int q4 = 0; q4 < DP / 64; ++q4) {
-                        const uint4 w = lds128(ks + r * RB + piece<RB, true>(r, q4 * 4 + tq) * 16);
-                        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma_16816<false>(x[n], qf[q4 * 4 + k][0], qf[q4 * 4 + k][1], qf[q4 * 4 + k][2],
-                                             qf[q4 * 4 + k][3], e4m3x2_to_f16x2((uint16_t)(ww[k] & 0xffffu)),
-                                             e4m3x2_to_f16x2((uint16_t)(ww[k] >> 16)));
+                    for (int n = 0; n < NX; ++n) {
+                        const uint4 v = lds128(ks + piece<C>(tok + token_of<C>(n, lr), q4 * 4 + tq));
+                        w[n][0] = v.x; w[n][1] = v.y; w[n][2] = v.z; w[n][3] = v.w;
                     }
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+#pragma unroll
+                        for (int n = 0; n < NX; ++n) {
+                            const uint32_t(&q)[4] = qf[q4 * 4 + k];
+                            uint32_t b0, b1;
+                            e4m3x4_to_f16x2(w[n][k], b0, b1);
+                            mma_16816<false>(x[n], q[0], q[1], q[2], q[3], b0, b1);
+                        }
                 }
             }
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+            for (int n = 0; n < NX; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) x[n][e] *= xs[e >> 1];
-            if (ok != 0xffffu || ragged) {
+                for (int k = 0; k < 2 * E; ++k) x[n][k] *= xs[k >> 1];
+            if (ok != kAll || ragged) {
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
+                for (int n = 0; n < NX; ++n)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int col = n * 8 + 2 * tq + (e & 1), j = j0 + col;
-                        const bool seen = ((ok >> col) & 1) && j <= hi[e >> 1] && j > lo[e >> 1];
-                        if (!seen) x[n][e] = -INFINITY;
+                    for (int k = 0; k < 2 * E; ++k) {
+                        const int t = token_of<C>(n, 2 * tq + (k & 1)), j = j0 + t;
+                        const bool seen = ((ok >> t) & 1) && j <= hi[k >> 1] && j > lo[k >> 1];
+                        if (!seen) x[n][k] = -INFINITY;
                     }
             }
 
             // running maximum and sum
-            float mn[2];
+            float mn[E];
+            bool up = false;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float t = fmaxf(fmaxf(x[0][2 * e], x[0][2 * e + 1]), fmaxf(x[1][2 * e], x[1][2 * e + 1]));
+            for (int e = 0; e < E; ++e) {
+                float t = fmaxf(x[0][2 * e], x[0][2 * e + 1]);
+#pragma unroll
+                for (int n = 1; n < NX; ++n) t = fmaxf(t, fmaxf(x[n][2 * e], x[n][2 * e + 1]));
                 t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 1));
                 t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 2));
                 mn[e] = fmaxf(m[e], t);
+                up = up || mn[e] > m[e];
             }
-            if (__any_sync(0xffffffffu, mn[0] > m[0] || mn[1] > m[1])) {
+            if (__any_sync(0xffffffffu, up)) {
+                float f[E];
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float f = ex2_approx(m[e] - (mn[e] == -INFINITY ? 0.f : mn[e]));
+                for (int e = 0; e < E; ++e) {
+                    f[e] = ex2_approx(m[e] - (mn[e] == -INFINITY ? 0.f : mn[e]));
                     m[e] = mn[e];
-                    l[e] *= f;
-#pragma unroll
-                    for (int n = 0; n < C::DW / 8; ++n) {
-                        o[n][2 * e] *= f;
-                        o[n][2 * e + 1] *= f;
-                    }
+                    l[e] *= f[e];
                 }
+#pragma unroll
+                for (int n = 0; n < C::DW / 8; ++n)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) o[n][k] *= f[(k >> 1) % E];
             }
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
+            for (int e = 0; e < E; ++e) {
                 const float mm = m[e] == -INFINITY ? 0.f : m[e];
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
+                for (int n = 0; n < NX; ++n)
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        x[n][2 * e + k] = ex2_approx(x[n][2 * e + k] - mm);
-                        l[e] += x[n][2 * e + k];
+                    for (int k = 2 * e; k < 2 * e + 2; ++k) {
+                        x[n][k] = ex2_approx(x[n][k] - mm);
+                        l[e] += x[n][k];
                     }
             }
 
-            // times the values: the probabilities, rounded to the 16-bit type of the product
-            // (off by 2^-8 of it at most for bf16, 2^-11 for fp16, to nearest, so over many tokens well
-            // below the rounding of the output); l keeps them unrounded
-            const uint32_t p0 = pack16<BF16>(x[0][0], x[0][1]), p1 = pack16<BF16>(x[0][2], x[0][3]);
-            const uint32_t p2 = pack16<BF16>(x[1][0], x[1][1]), p3 = pack16<BF16>(x[1][2], x[1][3]);
-            const int vr = tok + (lane & 15);
-            const uint32_t vrow = vs + vr * RB;
+            if (ok != kAll) {
+                // what was fetched along with the tokens (or left in the stage) is no value:
+                // nothing, so that weight 0 times it is 0
+                for (int t = lane / C::HB / 4; t < C::STEP; t += 32 / C::HB / 4)
+                    if (!((ok >> t) & 1))
+                        for (int p = lane % (C::HB * 4); p < C::RB / 16; p += C::HB * 4)
+                            sts128_zero(vs + piece<C>(tok + t, p));
+                sm100::fence_proxy_async_smem();
+                __syncwarp();
+            }
+            // Times the values: the probabilities rounded to the 16-bit type of the product (off
+            // by 2^-8 of it at most for bf16, 2^-11 for fp16, to nearest, so over many tokens well
+            // below the rounding of the output); l keeps them unrounded.
             auto values = [&](auto clean) {
                 // `clean`: infinities and NaN are taken out before the product, where a row must
                 // not meet the values of a token that another row sees
                 bool bad = false;
                 auto scrub = [&](uint32_t w) {
-                    if constexpr (!decltype(clean)::value) return w;
-                    const uint32_t E = BF16 ? 0x7f80u : 0x7c00u;
-                    if ((w & E) == E) { w &= 0xffff0000u; bad = true; }
-                    if ((w & (E << 16)) == E << 16) { w &= 0xffffu; bad = true; }
-                    return w;
+                    if constexpr (!decltype(clean)::value) {
+                        return w;
+                    } else if constexpr (KIND == kE4M3) {
+                        const uint32_t nan = __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                        bad = bad || nan;
+                        return w & ~nan;
+                    } else {
+                        const uint32_t nan = __vcmpeq2(w & (BF16 ? 0x7f807f80u : 0x7c007c00u),
+                                                       BF16 ? 0x7f807f80u : 0x7c007c00u);
+                        bad = bad || nan;
+                        return w & ~nan;
+                    }
                 };
+                uint32_t p[NX / 2][4];
+#pragma unroll
+                for (int u = 0; u < NX / 2; ++u)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        p[u][k] = pack16<BF16>(x[2 * u + k / 2][2 * (k & 1)], x[2 * u + k / 2][2 * (k & 1) + 1]);
                 if constexpr (KIND != kE4M3) {
+#pragma unroll
+                    for (int u = 0; u < NX / 2; ++u) {
+                        const int vr = tok + 16 * u + (lane & 15);
+#pragma unroll
+                        for (int n = 0; n < C::DW / 8; n += 2) {
+                            uint32_t b[4];
+                            ldmatrix_x4_trans(b, vs + piece<C>(vr, wd * (C::DW / 8) + n + (lane >> 4)));
+                            mma_16816<BF16>(o[n], p[u][0], p[u][1], p[u][2], p[u][3], scrub(b[0]), scrub(b[1]));
+                            mma_16816<BF16>(o[n + 1], p[u][0], p[u][1], p[u][2], p[u][3], scrub(b[2]), scrub(b[3]));
+                        }
+                    }
+                } else {
+                    const int vr = tok + token_of<C>(2 * (lane >> 4) + ((lane >> 1) & 1),
+                                                     2 * ((lane >> 2) & 3) + (lane & 1));
 #pragma unroll
                     for (int n = 0; n < C::DW / 8; n += 2) {
                         uint32_t b[4];
-                        ldmatrix_x4_trans(b, vrow + piece<RB, false>(vr, wd * (C::DW / 8) + n + (lane >> 4)) * 16);
-                        mma_16816<BF16>(o[n], p0, p1, p2, p3, scrub(b[0]), scrub(b[1]));
-                        mma_16816<BF16>(o[n + 1], p0, p1, p2, p3, scrub(b[2]), scrub(b[3]));
-                    }
-                } else {
+                        ldmatrix_b8_x2_trans(b, vs + piece<C>(vr, wd * (C::DW / 16) + n / 2));
 #pragma unroll
-                    for (int n = 0; n < C::DW / 8; n += 4) {
-                        // a piece holds 16 dimensions: as pairs of bytes, ldmatrix hands thread
-                        // (lr, tq) dimensions 2 lr, 2 lr + 1 of tokens 2 tq, 2 tq + 1
-                        uint32_t b[4];
-                        ldmatrix_x4_trans(b, vrow + piece<RB, false>(vr, wd * (C::DW / 16) + n / 2 + (lane >> 4)) * 16);
+                        for (int u = 0; u < 2; ++u)
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const uint32_t w0 = __byte_perm(b[2 * k], 0, 0x3120);
-                            const uint32_t w1 = __byte_perm(b[2 * k + 1], 0, 0x3120);
-                            mma_16816<false>(o[n + 2 * k], p0, p1, p2, p3,
-                                             scrub(e4m3x2_to_f16x2((uint16_t)(w0 & 0xffffu))),
-                                             scrub(e4m3x2_to_f16x2((uint16_t)(w1 & 0xffffu))));
-                            mma_16816<false>(o[n + 2 * k + 1], p0, p1, p2, p3,
-                                             scrub(e4m3x2_to_f16x2((uint16_t)(w0 >> 16))),
-                                             scrub(e4m3x2_to_f16x2((uint16_t)(w1 >> 16))));
-                        }
+                            for (int k = 0; k < 2; ++k) {
+                                uint32_t b0, b1;
+                                e4m3x4_to_f16x2(scrub(b[2 * u + k]), b0, b1);
+                                mma_16816<false>(o[n + k], p[u][0], p[u][1], p[u][2], p[u][3], b0, b1);
+                            }
                     }
                 }
                 return bad;
@@ -586,148 +643,125 @@ paged_attn_kernel(const GdnAttnArgs a, const int RT, Split *const splits, const 
                 values(std::false_type{});
             } else if (__any_sync(0xffffffffu, values(std::true_type{}))) {
                 // the taken-out values, for the rows that do see them
+#pragma unroll
+                for (int nj = 0; nj < NX; ++nj)
 #pragma unroll 1
-                for (int jj = 0; jj < 16; ++jj) {
-                    const int src = (lane & ~3) | ((jj & 7) >> 1);
-                    float p[2];
+                    for (int jj = 0; jj < 8; ++jj) {
+                        const int src = (lane & ~3) | (jj >> 1), tj = token_of<C>(nj, jj), j = j0 + tj;
+                        float p[E];
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float y0 = jj < 8 ? x[0][2 * e] : x[1][2 * e];
-                        const float y1 = jj < 8 ? x[0][2 * e + 1] : x[1][2 * e + 1];
-                        p[e] = __shfl_sync(0xffffffffu, (jj & 1) ? y1 : y0, src);
+                        for (int e = 0; e < E; ++e)
+                            p[e] = __shfl_sync(0xffffffffu, (jj & 1) ? x[nj][2 * e + 1] : x[nj][2 * e], src);
+                        if (!((ok >> tj) & 1)) continue;
+                        const unsigned char *const vb = smem + st * 2 * kHalfStage + kHalfStage;
+#pragma unroll
+                        for (int n = 0; n < C::DW / 8; ++n)
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const int at = (wd * C::DW + n * 8 + 2 * tq + k) * C::ESZ;
+                                const unsigned char *const e0 = vb + piece<C>(tok + tj, at / 16) + at % 16;
+                                float v;
+                                if constexpr (KIND == kBF16)
+                                    v = __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t *>(e0) << 16);
+                                else if constexpr (KIND == kF16)
+                                    v = __half2float(__ushort_as_half(*reinterpret_cast<const uint16_t *>(e0)));
+                                else
+                                    v = (*e0 & 0x7f) == 0x7f ? __uint_as_float(0x7fc00000u) : 0.f;
+                                if (isfinite(v)) continue;
+#pragma unroll
+                                for (int e = 0; e < E; ++e)
+                                    if (j <= hi[e] && j > lo[e]) o[n][2 * e + k] += p[e] * v;
+                            }
                     }
-                    const int j = j0 + jj;
-                    if (!((ok >> jj) & 1)) continue;
-                    const unsigned char *const vb = s_stage + (i % kStages) * 2 * kHalfStage + kHalfStage +
-                                                    (tok + jj) * RB;
-#pragma unroll
-                    for (int n = 0; n < C::DW / 8; ++n)
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const int dd = wd * C::DW + (KIND == kE4M3 ? (n & ~1) * 8 + 4 * tq + 2 * k + (n & 1)
-                                                                       : n * 8 + 2 * tq + k);
-                            const int at = dd * C::ESZ;
-                            const unsigned char *const e0 = vb + piece<RB, false>(tok + jj, at / 16) * 16 + at % 16;
-                            float v;
-                            if constexpr (KIND == kBF16)
-                                v = __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t *>(e0) << 16);
-                            else if constexpr (KIND == kF16)
-                                v = __half2float(__ushort_as_half(*reinterpret_cast<const uint16_t *>(e0)));
-                            else
-                                v = (*e0 & 0x7f) == 0x7f ? __uint_as_float(0x7fc00000u) : 0.f;
-                            if (isfinite(v)) continue;
-#pragma unroll
-                            for (int e = 0; e < 2; ++e)
-                                if (j <= hi[e] && j > lo[e]) o[n][2 * e + k] += p[e] * v;
-                        }
-                }
             }
         }
+        __syncwarp();
+        if (lane == 0) sm100::mbar_arrive(empty0 + 8 * st);
 
         if (d.tile == d.nt - 1 || i == n_tiles - 1) {   // the unit, or its part here, is done
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
+            for (int e = 0; e < E; ++e) {
                 l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
                 l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
             }
+            if constexpr (KIND == kE4M3) {
+                const float vsc = kv.v_scale ? __ldg(kv.v_scale + h) : 1.f;
+#pragma unroll
+                for (int n = 0; n < C::DW / 8; ++n)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) o[n][k] *= vsc;
+            }
             // the other warps of the same rows and dimensions join into wt = 0, one after the other
             constexpr int kWriters = WR * C::WD;
-            constexpr int kRegs = C::DW / 2;
+            constexpr int kRegs = C::DW / 4 * E;
             constexpr int kAtOnce = kRegs < 64 / kWriters ? kRegs : 64 / kWriters;
 #pragma unroll 1
             for (int src = 1; src < C::WT; ++src) {
-                float f0[2] = {1.f, 1.f}, f1[2] = {0.f, 0.f};
+                float f0[E], f1[E];
                 float *const buf = s_merge + (warp % kWriters) * kAtOnce * 32 + lane;
 #pragma unroll
                 for (int part = 0; part < kRegs / kAtOnce; ++part) {
                     if (wt == src) {
-                        if (part == 0) s_stat[warp % kWriters][lane] = make_float4(m[0], m[1], l[0], l[1]);
+                        if (part == 0)
+                            s_stat[warp % kWriters][lane] = make_float4(m[0], m[E - 1], l[0], l[E - 1]);
 #pragma unroll
                         for (int k = 0; k < kAtOnce; ++k) {
                             const int g = part * kAtOnce + k;
-                            buf[k * 32] = o[g / 4][g % 4];
+                            buf[k * 32] = o[g / (2 * E)][g % (2 * E)];
                         }
                     }
-                    __syncthreads();
+                    sm100::named_sync(1, kConsumers);
                     if (wt == 0) {
                         if (part == 0) {
                             const float4 y = s_stat[warp % kWriters][lane];
-                            const float ym[2] = {y.x, y.y}, yl[2] = {y.z, y.w};
 #pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const float mx = fmaxf(m[e], ym[e]), ms = mx == -INFINITY ? 0.f : mx;
+                            for (int e = 0; e < E; ++e) {
+                                const float ym = e ? y.y : y.x, yl = e ? y.w : y.z;
+                                const float mx = fmaxf(m[e], ym), ms = mx == -INFINITY ? 0.f : mx;
                                 f0[e] = ex2_approx(m[e] - ms);
-                                f1[e] = ex2_approx(ym[e] - ms);
+                                f1[e] = ex2_approx(ym - ms);
                                 m[e] = mx;
-                                l[e] = l[e] * f0[e] + yl[e] * f1[e];
+                                l[e] = l[e] * f0[e] + yl * f1[e];
                             }
                         }
 #pragma unroll
                         for (int k = 0; k < kAtOnce; ++k) {
-                            const int g = part * kAtOnce + k, e = (g >> 1) & 1;
-                            o[g / 4][g % 4] = o[g / 4][g % 4] * f0[e] + buf[k * 32] * f1[e];
+                            const int g = part * kAtOnce + k, e = g % (2 * E) / 2;
+                            o[g / (2 * E)][g % (2 * E)] = o[g / (2 * E)][g % (2 * E)] * f0[e] + buf[k * 32] * f1[e];
                         }
                     }
-                    __syncthreads();
+                    sm100::named_sync(1, kConsumers);
                 }
             }
             const bool whole = seg_tile == 0 && d.tile == d.nt - 1;
-            const int slot2 = seg_tile > 0 ? 0 : 1;
             if (wt == 0) {
-                const float vsc = KIND == kE4M3 && kv.v_scale ? __ldg(kv.v_scale + h) : 1.f;
-                if (whole) {
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int r = rt * C::RMAX + wr * 16 + lr + 8 * e;
+                for (int e = 0; e < E; ++e) {
+                    const int rl = wr * 16 + lr + 8 * e, r = rt * C::RMAX + rl;
+                    if (whole) {
                         if (r >= rows_all) continue;
                         const int t = r / group, hq = h * group + r - t * group;
                         const int64_t row = ((int64_t)d.b * a.T + t) * a.Hq + hq;
-                        const int64_t total = (int64_t)a.B * a.T * a.Hq;
-                        if (!in_range(row, 1, total, a.dev_status)) continue;
-                        const float inv = l[e] == 0.f ? 0.f : vsc / l[e];
+                        if (!in_range(row, 1, (int64_t)a.B * a.T * a.Hq, a.dev_status)) continue;
+                        const float inv = l[e] == 0.f ? 0.f : 1.f / l[e];
                         uint16_t *const out = static_cast<uint16_t *>(a.out) + row * D;
-                        if constexpr (KIND != kE4M3) {
 #pragma unroll
-                            for (int n = 0; n < C::DW / 8; ++n) {
-                                const int dd = wd * C::DW + n * 8 + 2 * tq;
-                                if (dd < D)
-                                    *reinterpret_cast<uint32_t *>(out + dd) =
-                                        pack16<BF16>(o[n][2 * e] * inv, o[n][2 * e + 1] * inv);
-                            }
-                        } else {
-#pragma unroll
-                            for (int n = 0; n < C::DW / 8; n += 2) {
-                                const int dd = wd * C::DW + n * 8 + 4 * tq;
-                                if (dd < D) {
-                                    uint32_t *const w = reinterpret_cast<uint32_t *>(out + dd);
-                                    w[0] = pack_out(a.q_bf16, o[n][2 * e] * inv, o[n + 1][2 * e] * inv);
-                                    w[1] = pack_out(a.q_bf16, o[n][2 * e + 1] * inv, o[n + 1][2 * e + 1] * inv);
-                                }
-                            }
+                        for (int n = 0; n < C::DW / 8; ++n) {
+                            const int dd = wd * C::DW + n * 8 + 2 * tq;
+                            if (dd < D)
+                                *reinterpret_cast<uint32_t *>(out + dd) =
+                                    pack_out(KIND == kE4M3 ? a.q_bf16 : BF16, o[n][2 * e] * inv, o[n][2 * e + 1] * inv);
                         }
                         if (a.lse && wd == 0 && tq == 0)
                             a.lse[row] = l[e] == 0.f ? -INFINITY : (m[e] + log2f(l[e])) * kLn2;
-                    }
-                } else {
-                    const int64_t p = (int64_t)c * 2 + slot2;
+                    } else {
+                        const int64_t p = ((int64_t)c * 2 + (seg_tile > 0 ? 0 : 1)) * C::RMAX + rl;
+                        if (!in_range(p, 1, (int64_t)G * 2 * C::RMAX, a.dev_status)) continue;
+                        if (wd == 0 && tq == 0) part_ml[p] = make_float2(m[e], l[e]);
+                        float *const po = part_o + p * DP + wd * C::DW;
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int64_t r = p * C::RMAX + wr * 16 + lr + 8 * e;
-                        if (!in_range(r, 1, (int64_t)G * 2 * C::RMAX, a.dev_status)) continue;
-                        if (wd == 0 && tq == 0) part_ml[r] = make_float2(m[e], l[e]);
-                        float *const po = part_o + r * DP + wd * C::DW;
-                        if constexpr (KIND != kE4M3) {
-#pragma unroll
-                            for (int n = 0; n < C::DW / 8; ++n)
-                                *reinterpret_cast<float2 *>(po + n * 8 + 2 * tq) =
-                                    make_float2(o[n][2 * e], o[n][2 * e + 1]);
-                        } else {
-#pragma unroll
-                            for (int n = 0; n < C::DW / 8; n += 2)
-                                *reinterpret_cast<float4 *>(po + n * 8 + 4 * tq) =
-                                    make_float4(o[n][2 * e] * vsc, o[n + 1][2 * e] * vsc,
-                                                o[n][2 * e + 1] * vsc, o[n + 1][2 * e + 1] * vsc);
-                        }
+                        for (int n = 0; n < C::DW / 8; ++n)
+                            *reinterpret_cast<float2 *>(po + n * 8 + 2 * tq) = make_float2(o[n][2 * e], o[n][2 * e + 1]);
                     }
                 }
             }
@@ -744,19 +778,24 @@ paged_attn_kernel(const GdnAttnArgs a, const int RT, Split *const splits, const 
                 }
             }
         }
-        if (more) note(i + 3, next);
     }
-    cp_async_wait<0>();
 }
 
-// One block joins one row of one unit that several blocks worked on.
+// One block joins one row of one unit that several blocks worked on: sixteen groups of threads
+// take every sixteenth part, DP / 4 threads of four dimensions each.
+constexpr int kJoinGroups = 16;
+constexpr int kMaxBlocks = 1024;
+
 template <int DP>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kJoinGroups *DP / 4)
 paged_attn_join_kernel(const GdnAttnArgs a, const int RT, const int RMAX, const Split *const splits,
                        const float2 *const part_ml, const float *const part_o)
 {
+    constexpr int kJoin = kJoinGroups * DP / 4;
+    __shared__ float s_w[kMaxBlocks];                   // maxima, then weights, of the parts
+    __shared__ float s_red[2][kJoin / 32];
+    __shared__ float4 s_o[kJoinGroups][DP / 4];
     wait_primary();
-    __shared__ float s_o[4][DP];
     const Split sp = splits[blockIdx.x];
     if (sp.c1 < 0) return;
     const int H = a.cache.heads, D = a.cache.head_dim, group = a.Hq / H;
@@ -768,65 +807,104 @@ paged_attn_join_kernel(const GdnAttnArgs a, const int RT, const int RMAX, const 
     // part k: the first block's is its second, the others' are their first
     auto at = [&](int k) { return ((int64_t)(sp.c0 + k) * 2 + (k == 0 ? 1 : 0)) * RMAX + rl; };
 
+    // the values come first: they do not depend on the weights
+    const int grp = tid / (DP / 4), d4 = tid % (DP / 4);
+    constexpr int kAhead = 4;
+    float4 y[kAhead];
+    auto fetch = [&](int k0) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int k = k0 + u * kJoinGroups;
+            y[u] = k < np ? __ldcg(reinterpret_cast<const float4 *>(part_o + at(k) * DP) + d4)
+                          : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+    };
+    fetch(grp);
     float top = -INFINITY;
-    for (int k = lane; k < np; k += 32) top = fmaxf(top, part_ml[at(k)].x);
+    constexpr int kMl = kMaxBlocks / kJoin;             // np <= kMaxBlocks
+    float2 ml[kMl];
+#pragma unroll
+    for (int u = 0; u < kMl; ++u) {
+        const int k = tid + u * kJoin;
+        ml[u] = k < np ? __ldcg(part_ml + at(k)) : make_float2(-INFINITY, 0.f);
+        top = fmaxf(top, ml[u].x);
+    }
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+    if (lane == 0) s_red[0][warp] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kJoin / 32; ++w) top = fmaxf(top, s_red[0][w]);
     const float ms = top == -INFINITY ? 0.f : top;
     float sum = 0.f;
-    for (int k = lane; k < np; k += 32) {
-        const float2 ml = part_ml[at(k)];
-        sum += ml.y * ex2_approx(ml.x - ms);
-    }
-    sum = gdn::warp_sum(sum);
-
-    constexpr int PER = DP / 32;
-    float acc[PER] = {};
-#pragma unroll 4
-    for (int k = warp; k < np; k += 4) {
-        const float w = ex2_approx(part_ml[at(k)].x - ms);
-        const float2 *const src = reinterpret_cast<const float2 *>(part_o + at(k) * DP) + lane;
 #pragma unroll
-        for (int e = 0; e < PER / 2; ++e) {
-            const float2 y = src[e * 32];
-            acc[2 * e] += w * y.x;
-            acc[2 * e + 1] += w * y.y;
+    for (int u = 0; u < kMl; ++u) {
+        const int k = tid + u * kJoin;
+        const float w = ex2_approx(ml[u].x - ms);
+        if (k < np) {
+            s_w[k] = w;
+            sum += ml[u].y * w;
         }
     }
+    sum = gdn::warp_sum(sum);
+    if (lane == 0) s_red[1][warp] = sum;
+    __syncthreads();
+    sum = 0.f;
 #pragma unroll
-    for (int e = 0; e < PER / 2; ++e) {
-        s_o[warp][e * 64 + 2 * lane] = acc[2 * e];
-        s_o[warp][e * 64 + 2 * lane + 1] = acc[2 * e + 1];
+    for (int w = 0; w < kJoin / 32; ++w) sum += s_red[1][w];
+
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k0 = grp; k0 < np; k0 += kAhead * kJoinGroups) {
+        if (k0 != grp) fetch(k0);
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int k = k0 + u * kJoinGroups;
+            if (k >= np) break;
+            const float w = s_w[k];
+            acc.x += w * y[u].x;
+            acc.y += w * y[u].y;
+            acc.z += w * y[u].z;
+            acc.w += w * y[u].w;
+        }
     }
+    s_o[grp][d4] = acc;
     __syncthreads();
     const int t = r / group, hq = h * group + r - t * group;
     const int64_t row = ((int64_t)sp.b * a.T + t) * a.Hq + hq;
     if (!in_range(row, 1, (int64_t)a.B * a.T * a.Hq, a.dev_status)) return;
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    for (int w = tid; w < D / 2; w += kThreads) {
-        float y[2];
+    if (tid < D / 4) {
+        acc = s_o[0][tid];
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-            y[e] = (s_o[0][2 * w + e] + s_o[1][2 * w + e] + s_o[2][2 * w + e] + s_o[3][2 * w + e]) * inv;
-        reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.out) + row * D)[w] = pack_out(a.q_bf16, y[0], y[1]);
+        for (int g = 1; g < kJoinGroups; ++g) {
+            const float4 z = s_o[g][tid];
+            acc.x += z.x;
+            acc.y += z.y;
+            acc.z += z.z;
+            acc.w += z.w;
+        }
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        uint32_t *const out = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.out) + row * D) + 2 * tid;
+        out[0] = pack_out(a.q_bf16, acc.x * inv, acc.y * inv);
+        out[1] = pack_out(a.q_bf16, acc.z * inv, acc.w * inv);
     }
     if (a.lse && tid == 0) a.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
 
 // ------------------------------------------------------------------ host
 int padded(int D) { return D <= 64 ? 64 : (D <= 128 ? 128 : 256); }
-// warps over rows: as few as hold them; a 256-wide head leaves registers for 32 rows
+// warps over rows: as few as hold them; 256-wide heads leave room for two
 int row_warps(int rows, int DP) { return rows <= 16 ? 1 : (rows <= 32 || DP == 256 ? 2 : 4); }
-int max_blocks() { return 2 * sm_count(); }
+int max_blocks() { return std::min(2 * sm_count(), kMaxBlocks); }
 
 struct Layout {
     int RT, RMAX, n_splits;
     uint64_t ml_at, o_at, bytes;
 };
 
-Layout layout(int B, int T, int Hq, int H, int D, int blocks)
+// `DP` as the kernel pads the head
+Layout layout(int B, int T, int Hq, int H, int DP, int blocks)
 {
-    const int DP = padded(D), rows = T * (Hq / H);
+    const int rows = T * (Hq / H);
     Layout y;
     y.RMAX = 16 * row_warps(rows, DP);
     y.RT = (rows + y.RMAX - 1) / y.RMAX;
@@ -838,39 +916,107 @@ Layout layout(int B, int T, int Hq, int H, int D, int blocks)
     return y;
 }
 
+PFN_cuTensorMapEncodeTiled_v12000 get_encode()
+{
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    }();
+    return fn;
+}
+
+// keys or values as (dimension, token of a page, head, page), in boxes of `box` tokens of a head
+cudaError_t encode(CUtensorMap *map, const void *base, const gdn_paged_cache &kv, int es, int row_bytes, int box)
+{
+    const PFN_cuTensorMapEncodeTiled_v12000 fn = get_encode();
+    if (!fn) return cudaErrorNotSupported;
+    const cuuint64_t dims[4] = {(cuuint64_t)kv.head_dim, (cuuint64_t)kv.page_size, (cuuint64_t)kv.heads,
+                                (cuuint64_t)kv.num_pages};
+    const cuuint64_t none = (cuuint64_t)kv.head_dim * es;   // the stride of a dimension of one
+    const cuuint64_t strides[3] = {kv.page_size > 1 ? (cuuint64_t)kv.token_stride * es : none,
+                                   kv.heads > 1 ? (cuuint64_t)kv.head_stride * es : none,
+                                   kv.num_pages > 1 ? (cuuint64_t)kv.page_stride * es : none};
+    const int inner = row_bytes < 128 ? row_bytes : 128;
+    const cuuint32_t boxes[4] = {(cuuint32_t)(inner / es), (cuuint32_t)box, 1, 1};
+    const cuuint32_t steps[4] = {1, 1, 1, 1};
+    // whole tokens side by side are fetched 256 bytes at a time; the rows of one head between
+    // those of others no further than they reach
+    const int reach = kv.page_size > 1 && kv.token_stride != kv.head_dim ? kv.head_dim * es : 256;
+    const CUtensorMapL2promotion l2 = reach % 256 == 0   ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                                      : reach % 128 == 0 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                                                         : CU_TENSOR_MAP_L2_PROMOTION_L2_64B;
+    const CUresult r = fn(map, es == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 4,
+                          const_cast<void *>(base), dims, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          inner == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                          l2, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// tokens of a box: the largest power of two that divides the page size, a tile's at most
+int box_tokens(int page_size, int tile)
+{
+    const int p = page_size & -page_size;
+    return p < tile ? p : tile;
+}
+
 template <int KIND, int DP, int WR>
 cudaError_t launch(const GdnAttnArgs &a, cudaStream_t stream)
 {
     using C = Cfg<KIND, DP, WR>;
     static DeviceOnce once;
     cudaError_t e = once.run([] {
+        // the warps that compute wait for registers that the block must have been launched with
+        cudaFuncAttributes at;
+        cudaError_t e = cudaFuncGetAttributes(&at, paged_attn_kernel<KIND, DP, WR>);
+        if (e != cudaSuccess) return e;
+        if (at.numRegs * 2 < kFetchRegs + kComputeRegs) return cudaErrorInvalidKernelImage;
         return cudaFuncSetAttribute(paged_attn_kernel<KIND, DP, WR>,
                                     cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     });
     if (e != cudaSuccess) return e;
     const gdn_paged_cache &kv = a.cache;
-    const Layout y = layout(a.B, a.T, a.Hq, kv.heads, kv.head_dim, max_blocks());
+    const int box = box_tokens(kv.page_size, C::TILE);
+    CUtensorMap kmap, vmap;
+    e = encode(&kmap, kv.k, kv, C::ESZ, C::RB, box);
+    if (e == cudaSuccess) e = encode(&vmap, kv.v, kv, C::ESZ, C::RB, box);
+    if (e != cudaSuccess) return e;
+    const Layout y = layout(a.B, a.T, a.Hq, kv.heads, DP, max_blocks());
     // no more blocks than there can be tiles
     const int64_t cap = (int64_t)kv.width * kv.page_size;
-    const double tiles = (double)a.B * kv.heads * y.RT * (double)((cap + C::TILE - 1) / C::TILE);
-    const int blocks = tiles < max_blocks() ? (tiles < 1 ? 1 : (int)tiles) : max_blocks();
+    const double tiles = (double)a.B * kv.heads * y.RT * (double)((cap + C::TILE - 1) / C::TILE + 1);
+    const int blocks = tiles < max_blocks() ? (int)tiles : max_blocks();
     unsigned char *const ws = static_cast<unsigned char *>(a.workspace);
     Split *const splits = reinterpret_cast<Split *>(ws);
     float2 *const ml = reinterpret_cast<float2 *>(ws + y.ml_at);
     float *const o = reinterpret_cast<float *>(ws + y.o_at);
     const int64_t units = (int64_t)a.B * kv.heads * y.RT;
     const int n_splits = (int)(units < blocks ? units : blocks);
-    paged_attn_kernel<KIND, DP, WR><<<blocks, kThreads, C::SMEM, stream>>>(a, y.RT, splits, n_splits, ml, o);
+    paged_attn_kernel<KIND, DP, WR><<<blocks, kThreads, C::SMEM, stream>>>(kmap, vmap, a, box, y.RT, splits,
+                                                                           n_splits, ml, o);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_dependent(paged_attn_join_kernel<DP>, dim3(n_splits, y.RMAX), dim3(kThreads), 0,
-                            stream, a, y.RT, y.RMAX, splits, ml, o);
+    const int rows = std::min(y.RMAX, a.T * (a.Hq / kv.heads));
+    return launch_dependent(paged_attn_join_kernel<DP>, dim3(n_splits, rows), dim3(kJoinGroups * DP / 4), 0, stream,
+                            a, y.RT, y.RMAX, splits, ml, o);
+}
+
+// A box starts on 128 bytes of shared memory: 64-byte rows need an even number of tokens, so
+// 8-bit heads of at most 64 dimensions on pages of an odd number of tokens run 128 wide (the
+// dimensions past the head's are zeros).
+int padded(const gdn_paged_cache &kv)
+{
+    const bool odd64 = kv.dtype == GDN_E4M3 && kv.head_dim <= 64 && kv.page_size % 2 != 0;
+    return odd64 ? 128 : padded(kv.head_dim);
 }
 
 template <int KIND>
 cudaError_t dispatch(const GdnAttnArgs &a, cudaStream_t stream)
 {
-    const int DP = padded(a.cache.head_dim);
+    const int DP = padded(a.cache);
     const int WR = row_warps(a.T * (a.Hq / a.cache.heads), DP);
     switch (DP + WR) {
     case 64 + 1: return launch<KIND, 64, 1>(a, stream);
@@ -904,9 +1050,12 @@ int gdn_cache::sm_count()
 uint64_t paged_attn_workspace_bytes(int32_t B, int32_t T, int32_t Hq, int32_t heads, int32_t D,
                                     int32_t cache_dtype)
 {
-    (void)cache_dtype;
-    const int blocks = gdn_attn::max_blocks();
-    return blocks == 0 ? 0 : gdn_attn::layout(B, T, Hq, heads, D, blocks).bytes;
+    using namespace gdn_attn;
+    const int blocks = max_blocks(), DP = padded(D);
+    if (blocks == 0) return 0;
+    // (8-bit heads of at most 64 dimensions may run 128 wide, by the page size)
+    const uint64_t n = layout(B, T, Hq, heads, DP, blocks).bytes;
+    return cache_dtype == GDN_E4M3 && DP == 64 ? std::max(n, layout(B, T, Hq, heads, 128, blocks).bytes) : n;
 }
 
 cudaError_t launch_paged_attn(const GdnAttnArgs &a, cudaStream_t stream)
