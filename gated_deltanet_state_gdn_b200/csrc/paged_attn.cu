@@ -88,6 +88,30 @@ struct Split {              // a unit whose parts lie in blocks [c0, c1]
     int u_lo, b, c0, c1;    // c1 < 0: nothing to join
 };
 
+// W tiles in a row dealt to G blocks: the first `more` get one more than the others
+struct Deal {
+    int64_t W;
+    int each, more;
+    __device__ __forceinline__ Deal(int64_t w, int G) : W(w)
+    {
+        if (w < ((int64_t)1 << 31)) {
+            each = (int)w / G;
+            more = (int)w - each * G;
+        } else {
+            each = (int)(w / G);
+            more = (int)(w - (int64_t)each * G);
+        }
+    }
+    __device__ __forceinline__ int64_t first(int c) const { return (int64_t)c * each + min(c, more); }
+    __device__ __forceinline__ int count(int c) const { return each + (c < more); }
+    __device__ __forceinline__ int owner(int64_t t) const
+    {
+        const int64_t long_ones = (int64_t)more * (each + 1);
+        if (t < long_ones) return (int)(t / (each + 1));
+        return more + (int)((t - long_ones) / each);
+    }
+};
+
 // rows of the batch: slot (or -1 for padding) and length
 struct RowInfo {
     int slot, len;
@@ -216,10 +240,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     constexpr bool BF16 = KIND == kBF16;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *const smem = smem_raw + (kAlign - (smem_u32(smem_raw) & (kAlign - 1))) % kAlign;
-    float *const s_merge = reinterpret_cast<float *>(smem + kStages * 2 * kHalfStage);
+    float4 *const s_merge = reinterpret_cast<float4 *>(smem + kStages * 2 * kHalfStage);
     __shared__ __align__(8) uint64_t s_full[kStages], s_empty[kStages];
     __shared__ int64_t s_sum[kThreads / 32];
-    __shared__ int64_t s_found[2];
+    __shared__ int s_found[3];
     __shared__ Desc s_desc[kStages];
     __shared__ uint32_t s_valid[kStages][TILE / 32];
     __shared__ float4 s_stat[2][32];
@@ -247,30 +271,34 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     }
 
     // ---- this block's run of tiles
-    int64_t S = 0;      // tiles of the batch, a unit of each request
+    int64_t S = 0, incl0;      // tiles of the batch, a unit of each request; up to this thread's
     const int nt0 = tid < a.B ? tiles_of<TILE>(a, row_info(a, tid, c == 0).len, box) : 0;
     {
         int64_t mine = nt0;
         for (int b = tid + kThreads; b < a.B; b += kThreads)
             mine += tiles_of<TILE>(a, row_info(a, b, c == 0).len, box);
-        block_scan(mine, s_sum, &S);
+        incl0 = block_scan(mine, s_sum, &S);
     }
-    const int64_t W = S * U;
-    const int64_t Ge = W < G ? W : G;
-    const int64_t t0 = c < Ge ? c * W / Ge : 0, t1 = c < Ge ? (c + 1) * W / Ge : 0;
-    const int n_tiles = (int)(t1 - t0);
+    const Deal deal(S * U, G);
+    const int64_t t0 = deal.first(c);
+    const int n_tiles = deal.count(c);
 
     // the request, unit and tile where it begins
     if (n_tiles > 0) {
         int64_t before = 0;
         for (int b0 = 0; b0 < a.B; b0 += kThreads) {
             const int b = b0 + tid;
-            const int nt = b0 == 0 ? nt0 : (b < a.B ? tiles_of<TILE>(a, row_info(a, b, false).len, box) : 0);
-            int64_t all;
-            const int64_t incl = before + block_scan(nt, s_sum, &all);
+            int nt = nt0;
+            int64_t incl = incl0, all = S;
+            if (a.B > kThreads) {       // the sum above was over more than a request a thread
+                nt = b < a.B ? tiles_of<TILE>(a, row_info(a, b, false).len, box) : 0;
+                incl = before + block_scan(nt, s_sum, &all);
+            }
             if (nt > 0 && t0 >= (incl - nt) * U && t0 < incl * U) {
+                const int64_t past = t0 - (incl - nt) * U;
                 s_found[0] = b;
-                s_found[1] = t0 - (incl - nt) * U;
+                s_found[1] = (int)(past / nt);
+                s_found[2] = (int)(past % nt);
             }
             before += all;
             if (t0 < before * U) break;
@@ -283,11 +311,11 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         registers_down<kFetchRegs>();
         const int fw = warp - kConsumers / 32;
         if (n_tiles == 0 || fw >= C::FETCH) return;
-        int cb = (int)s_found[0], win = cb;     // request; lane i knows about request win + i
+        int cb = s_found[0], win = cb;     // request; lane i knows about request win + i
         RowInfo mine = cb + lane < a.B ? row_info(a, cb + lane, false) : RowInfo{-1, 0};
         int len = __shfl_sync(0xffffffffu, mine.len, 0), slot = __shfl_sync(0xffffffffu, mine.slot, 0);
         int cnt = tiles_of<TILE>(a, len, box);
-        int cu = (int)(s_found[1] / cnt), ct = (int)(s_found[1] - (int64_t)cu * cnt);
+        int cu = s_found[1], ct = s_found[2];
         for (int i = 0; i < n_tiles; ++i) {
             const int st = i % kStages;
             const int base = first_tile(a, len, box) + ct * TILE, lo = first_seen(a, len);
@@ -691,44 +719,48 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
 #pragma unroll
                     for (int k = 0; k < 4; ++k) o[n][k] *= vsc;
             }
-            // the other warps of the same rows and dimensions join into wt = 0, one after the other
-            constexpr int kWriters = WR * C::WD;
-            constexpr int kRegs = C::DW / 4 * E;
-            constexpr int kAtOnce = kRegs < 64 / kWriters ? kRegs : 64 / kWriters;
-#pragma unroll 1
-            for (int src = 1; src < C::WT; ++src) {
-                float f0[E], f1[E];
-                float *const buf = s_merge + (warp % kWriters) * kAtOnce * 32 + lane;
+            // The other warps of the same rows and dimensions join into wt = 0, halving their
+            // number; rows 8 to 15 only where the unit has them (one or two writers of 4 KB).
+            constexpr int kQ = C::DW / 16;              // float4 of a row's
+            const bool two = rows_all - rt * C::RMAX - wr * 16 > 8;
 #pragma unroll
-                for (int part = 0; part < kRegs / kAtOnce; ++part) {
-                    if (wt == src) {
-                        if (part == 0)
-                            s_stat[warp % kWriters][lane] = make_float4(m[0], m[E - 1], l[0], l[E - 1]);
+            for (int half = C::WT / 2; half > 0; half >>= 1) {
+                float4 *const buf = s_merge + (warp % (half * WR * C::WD)) * kQ * 32 + lane;
+                float f0[2], f1[2];
 #pragma unroll
-                        for (int k = 0; k < kAtOnce; ++k) {
-                            const int g = part * kAtOnce + k;
-                            buf[k * 32] = o[g / (2 * E)][g % (2 * E)];
-                        }
+                for (int e = 0; e < 2; ++e) {
+                    if (e == 1 && rows_all - rt * C::RMAX <= 8) break;
+                    if (wt >= half && wt < 2 * half) {
+                        if (e == 0) s_stat[warp % (half * WR * C::WD)][lane] = make_float4(m[0], m[1], l[0], l[1]);
+                        if (e == 0 || two)
+#pragma unroll
+                            for (int k = 0; k < kQ; ++k)
+                                buf[k * 32] = make_float4(o[2 * k][2 * e], o[2 * k][2 * e + 1],
+                                                          o[2 * k + 1][2 * e], o[2 * k + 1][2 * e + 1]);
                     }
                     sm100::named_sync(1, kConsumers);
-                    if (wt == 0) {
-                        if (part == 0) {
-                            const float4 y = s_stat[warp % kWriters][lane];
+                    if (wt < half) {
+                        if (e == 0) {
+                            const float4 y = s_stat[warp % (half * WR * C::WD)][lane];
 #pragma unroll
-                            for (int e = 0; e < E; ++e) {
-                                const float ym = e ? y.y : y.x, yl = e ? y.w : y.z;
-                                const float mx = fmaxf(m[e], ym), ms = mx == -INFINITY ? 0.f : mx;
-                                f0[e] = ex2_approx(m[e] - ms);
-                                f1[e] = ex2_approx(ym - ms);
-                                m[e] = mx;
-                                l[e] = l[e] * f0[e] + yl * f1[e];
+                            for (int r = 0; r < 2; ++r) {
+                                const float ym = r ? y.y : y.x, yl = r ? y.w : y.z;
+                                const float mx = fmaxf(m[r], ym), ms = mx == -INFINITY ? 0.f : mx;
+                                f0[r] = ex2_approx(m[r] - ms);
+                                f1[r] = ex2_approx(ym - ms);
+                                m[r] = mx;
+                                l[r] = l[r] * f0[r] + yl * f1[r];
                             }
                         }
+                        if (e == 0 || two)
 #pragma unroll
-                        for (int k = 0; k < kAtOnce; ++k) {
-                            const int g = part * kAtOnce + k, e = g % (2 * E) / 2;
-                            o[g / (2 * E)][g % (2 * E)] = o[g / (2 * E)][g % (2 * E)] * f0[e] + buf[k * 32] * f1[e];
-                        }
+                            for (int k = 0; k < kQ; ++k) {
+                                const float4 y = buf[k * 32];
+                                o[2 * k][2 * e] = o[2 * k][2 * e] * f0[e] + y.x * f1[e];
+                                o[2 * k][2 * e + 1] = o[2 * k][2 * e + 1] * f0[e] + y.y * f1[e];
+                                o[2 * k + 1][2 * e] = o[2 * k + 1][2 * e] * f0[e] + y.z * f1[e];
+                                o[2 * k + 1][2 * e + 1] = o[2 * k + 1][2 * e + 1] * f0[e] + y.w * f1[e];
+                            }
                     }
                     sm100::named_sync(1, kConsumers);
                 }
@@ -769,7 +801,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             if (tid == 0 && seg_tile == 0) {
                 const int64_t unit = (int64_t)d.b * U + d.u;
                 const int64_t end = t0 + i + (d.nt - 1 - d.tile);   // the unit's last tile
-                const int last = (int)(((end + 1) * Ge - 1) / W);
+                const int last = deal.owner(end);
                 const int64_t at = by_unit ? unit : c;
                 if ((by_unit || !whole) && in_range(at, 1, n_splits, a.dev_status)) {
                     Split sp;
@@ -781,18 +813,21 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     }
 }
 
-// One block joins one row of one unit that several blocks worked on: sixteen groups of threads
-// take every sixteenth part, DP / 4 threads of four dimensions each.
+// Joins the rows of units that several blocks worked on, `per` rows a block.  Up to kFew parts of
+// a row are joined by one warp, eight rows side by side; more by the whole block, row by row,
+// sixteen groups of threads taking every sixteenth part.
 constexpr int kJoinGroups = 16;
 constexpr int kMaxBlocks = 1024;
+constexpr int kFew = 8;
+constexpr int kJoinRows = 8;
 
 template <int DP>
 __global__ void __launch_bounds__(kJoinGroups *DP / 4)
-paged_attn_join_kernel(const GdnAttnArgs a, const int RT, const int RMAX, const Split *const splits,
-                       const float2 *const part_ml, const float *const part_o)
+paged_attn_join_kernel(const GdnAttnArgs a, const int RT, const int RMAX, const int per,
+                       const Split *const splits, const float2 *const part_ml, const float *const part_o)
 {
     constexpr int kJoin = kJoinGroups * DP / 4;
-    __shared__ float s_w[kMaxBlocks];                   // maxima, then weights, of the parts
+    __shared__ float s_w[kMaxBlocks];                   // weights of the parts
     __shared__ float s_red[2][kJoin / 32];
     __shared__ float4 s_o[kJoinGroups][DP / 4];
     wait_primary();
@@ -800,94 +835,136 @@ paged_attn_join_kernel(const GdnAttnArgs a, const int RT, const int RMAX, const 
     if (sp.c1 < 0) return;
     const int H = a.cache.heads, D = a.cache.head_dim, group = a.Hq / H;
     const int h = sp.u_lo / RT, rt = sp.u_lo - h * RT;
-    const int rl = blockIdx.y, r = rt * RMAX + rl;
-    if (r >= a.T * group) return;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int np = sp.c1 - sp.c0 + 1;
+    const int rows = min(RMAX, a.T * group - rt * RMAX);        // of the unit
+    auto place = [&](int rl) {
+        const int r = rt * RMAX + rl, t = r / group;
+        return ((int64_t)sp.b * a.T + t) * a.Hq + h * group + r - t * group;
+    };
     // part k: the first block's is its second, the others' are their first
-    auto at = [&](int k) { return ((int64_t)(sp.c0 + k) * 2 + (k == 0 ? 1 : 0)) * RMAX + rl; };
+    auto at = [&](int k, int rl) { return ((int64_t)(sp.c0 + k) * 2 + (k == 0 ? 1 : 0)) * RMAX + rl; };
+    auto store = [&](int64_t row, int d, float4 y, float sum) {
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        uint32_t *const out = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.out) + row * D + d);
+        out[0] = pack_out(a.q_bf16, y.x * inv, y.y * inv);
+        out[1] = pack_out(a.q_bf16, y.z * inv, y.w * inv);
+    };
+    const int64_t all_rows = (int64_t)a.B * a.T * a.Hq;
 
-    // the values come first: they do not depend on the weights
+    if (per == kJoinRows && np <= kFew) {
+        for (int rl = blockIdx.y * per + warp; rl < min(rows, (int)(blockIdx.y + 1) * per); rl += kJoin / 32) {
+            float2 ml = make_float2(-INFINITY, 0.f);
+            if (lane < np) ml = __ldcg(part_ml + at(lane, rl));
+            float top = ml.x;
+#pragma unroll
+            for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+            const float ms = top == -INFINITY ? 0.f : top;
+            const float w = ex2_approx(ml.x - ms);
+            const float sum = gdn::warp_sum(ml.y * w);
+            const int64_t row = place(rl);
+            const bool ok = in_range(row, 1, all_rows, a.dev_status);
+            for (int d0 = 0; d0 < D; d0 += 128) {
+                const int d = d0 + 4 * lane;
+                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int k = 0; k < kFew; ++k) {
+                    const float wk = __shfl_sync(0xffffffffu, w, k);
+                    if (k < np && d < D) {
+                        const float4 y = __ldcg(reinterpret_cast<const float4 *>(part_o + at(k, rl) * DP + d));
+                        acc.x += wk * y.x;
+                        acc.y += wk * y.y;
+                        acc.z += wk * y.z;
+                        acc.w += wk * y.w;
+                    }
+                }
+                if (ok && d < D) store(row, d, acc, sum);
+            }
+            if (ok && a.lse && lane == 0) a.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+        }
+        return;
+    }
+
     const int grp = tid / (DP / 4), d4 = tid % (DP / 4);
     constexpr int kAhead = 4;
-    float4 y[kAhead];
-    auto fetch = [&](int k0) {
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            const int k = k0 + u * kJoinGroups;
-            y[u] = k < np ? __ldcg(reinterpret_cast<const float4 *>(part_o + at(k) * DP) + d4)
-                          : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-    };
-    fetch(grp);
-    float top = -INFINITY;
     constexpr int kMl = kMaxBlocks / kJoin;             // np <= kMaxBlocks
-    float2 ml[kMl];
+    for (int rl = blockIdx.y * per; rl < min(rows, (int)(blockIdx.y + 1) * per); ++rl) {
+        // the values come first: they do not depend on the weights
+        float4 y[kAhead];
+        auto fetch = [&](int k0) {
 #pragma unroll
-    for (int u = 0; u < kMl; ++u) {
-        const int k = tid + u * kJoin;
-        ml[u] = k < np ? __ldcg(part_ml + at(k)) : make_float2(-INFINITY, 0.f);
-        top = fmaxf(top, ml[u].x);
-    }
+            for (int u = 0; u < kAhead; ++u) {
+                const int k = k0 + u * kJoinGroups;
+                y[u] = k < np ? __ldcg(reinterpret_cast<const float4 *>(part_o + at(k, rl) * DP) + d4)
+                              : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+        };
+        fetch(grp);
+        float top = -INFINITY;
+        float2 ml[kMl];
 #pragma unroll
-    for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-    if (lane == 0) s_red[0][warp] = top;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kJoin / 32; ++w) top = fmaxf(top, s_red[0][w]);
-    const float ms = top == -INFINITY ? 0.f : top;
-    float sum = 0.f;
-#pragma unroll
-    for (int u = 0; u < kMl; ++u) {
-        const int k = tid + u * kJoin;
-        const float w = ex2_approx(ml[u].x - ms);
-        if (k < np) {
-            s_w[k] = w;
-            sum += ml[u].y * w;
+        for (int u = 0; u < kMl; ++u) {
+            const int k = tid + u * kJoin;
+            ml[u] = k < np ? __ldcg(part_ml + at(k, rl)) : make_float2(-INFINITY, 0.f);
+            top = fmaxf(top, ml[u].x);
         }
-    }
-    sum = gdn::warp_sum(sum);
-    if (lane == 0) s_red[1][warp] = sum;
-    __syncthreads();
-    sum = 0.f;
 #pragma unroll
-    for (int w = 0; w < kJoin / 32; ++w) sum += s_red[1][w];
+        for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+        if (lane == 0) s_red[0][warp] = top;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kJoin / 32; ++w) top = fmaxf(top, s_red[0][w]);
+        const float ms = top == -INFINITY ? 0.f : top;
+        float sum = 0.f;
+#pragma unroll
+        for (int u = 0; u < kMl; ++u) {
+            const int k = tid + u * kJoin;
+            const float w = ex2_approx(ml[u].x - ms);
+            if (k < np) {
+                s_w[k] = w;
+                sum += ml[u].y * w;
+            }
+        }
+        sum = gdn::warp_sum(sum);
+        if (lane == 0) s_red[1][warp] = sum;
+        __syncthreads();
+        sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kJoin / 32; ++w) sum += s_red[1][w];
 
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k0 = grp; k0 < np; k0 += kAhead * kJoinGroups) {
-        if (k0 != grp) fetch(k0);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k0 = grp; k0 < np; k0 += kAhead * kJoinGroups) {
+            if (k0 != grp) fetch(k0);
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            const int k = k0 + u * kJoinGroups;
-            if (k >= np) break;
-            const float w = s_w[k];
-            acc.x += w * y[u].x;
-            acc.y += w * y[u].y;
-            acc.z += w * y[u].z;
-            acc.w += w * y[u].w;
+            for (int u = 0; u < kAhead; ++u) {
+                const int k = k0 + u * kJoinGroups;
+                if (k >= np) break;
+                const float w = s_w[k];
+                acc.x += w * y[u].x;
+                acc.y += w * y[u].y;
+                acc.z += w * y[u].z;
+                acc.w += w * y[u].w;
+            }
         }
-    }
-    s_o[grp][d4] = acc;
-    __syncthreads();
-    const int t = r / group, hq = h * group + r - t * group;
-    const int64_t row = ((int64_t)sp.b * a.T + t) * a.Hq + hq;
-    if (!in_range(row, 1, (int64_t)a.B * a.T * a.Hq, a.dev_status)) return;
-    if (tid < D / 4) {
-        acc = s_o[0][tid];
+        s_o[grp][d4] = acc;
+        __syncthreads();
+        const int64_t row = place(rl);
+        const bool ok = in_range(row, 1, all_rows, a.dev_status);
+        if (ok && tid < D / 4) {
+            acc = s_o[0][tid];
 #pragma unroll
-        for (int g = 1; g < kJoinGroups; ++g) {
-            const float4 z = s_o[g][tid];
-            acc.x += z.x;
-            acc.y += z.y;
-            acc.z += z.z;
-            acc.w += z.w;
+            for (int g = 1; g < kJoinGroups; ++g) {
+                const float4 z = s_o[g][tid];
+                acc.x += z.x;
+                acc.y += z.y;
+                acc.z += z.z;
+                acc.w += z.w;
+            }
+            store(row, 4 * tid, acc, sum);
         }
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        uint32_t *const out = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.out) + row * D) + 2 * tid;
-        out[0] = pack_out(a.q_bf16, acc.x * inv, acc.y * inv);
-        out[1] = pack_out(a.q_bf16, acc.z * inv, acc.w * inv);
+        if (ok && a.lse && tid == 0) a.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+        __syncthreads();        // the shared arrays are used again
     }
-    if (a.lse && tid == 0) a.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
 
 // ------------------------------------------------------------------ host
@@ -999,9 +1076,12 @@ cudaError_t launch(const GdnAttnArgs &a, cudaStream_t stream)
                                                                            n_splits, ml, o);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
+    // Few units: many parts each, a block a row.  Many: two or three parts each as a rule, a warp a
+    // row and eight rows a block.
     const int rows = std::min(y.RMAX, a.T * (a.Hq / kv.heads));
-    return launch_dependent(paged_attn_join_kernel<DP>, dim3(n_splits, rows), dim3(kJoinGroups * DP / 4), 0, stream,
-                            a, y.RT, y.RMAX, splits, ml, o);
+    const int per = units * kFew >= blocks ? kJoinRows : 1;
+    return launch_dependent(paged_attn_join_kernel<DP>, dim3(n_splits, (rows + per - 1) / per),
+                            dim3(kJoinGroups * DP / 4), 0, stream, a, y.RT, y.RMAX, per, splits, ml, o);
 }
 
 // A box starts on 128 bytes of shared memory: 64-byte rows need an even number of tokens, so
