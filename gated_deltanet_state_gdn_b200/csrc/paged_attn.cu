@@ -81,14 +81,18 @@ struct Cfg {
 };
 
 struct Desc {
-    int b, u, base, len, tile, nt;
+    int b, u, base, len, tile, nt, last;    // last: of the block's run
+    int64_t place;                          // in the deal
 };
 
 struct Split {              // a unit whose parts lie in blocks [c0, c1]
     int u_lo, b, c0, c1;    // c1 < 0: nothing to join
 };
 
-// W tiles in a row dealt to G blocks: the first `more` get one more than the others
+// What a unit costs beside its tiles (its queries, its end), in tiles, when work is dealt out.
+constexpr int kUnitCost = 2;
+
+// W places in a row dealt to G blocks: the first `more` get one more than the others
 struct Deal {
     int64_t W;
     int each, more;
@@ -150,10 +154,11 @@ __device__ __forceinline__ int first_tile(const GdnAttnArgs &a, int len, int box
     return first_seen(a, len) & ~(box - 1);
 }
 
+// places of a unit in the deal: kUnitCost, then its tiles; none if it has no tile
 template <int TILE>
-__device__ __forceinline__ int tiles_of(const GdnAttnArgs &a, int len, int box)
+__device__ __forceinline__ int places_of(const GdnAttnArgs &a, int len, int box)
 {
-    return len > first_seen(a, len) ? (len - first_tile(a, len, box) + TILE - 1) / TILE : 0;
+    return len > first_seen(a, len) ? kUnitCost + (len - first_tile(a, len, box) + TILE - 1) / TILE : 0;
 }
 
 // inclusive prefix sum over the block's threads; *total is the same in all
@@ -178,9 +183,8 @@ __device__ __forceinline__ int64_t block_scan(int64_t x, int64_t *s, int64_t *to
     return x;
 }
 
-// Wait for a phase of a barrier, about a second at most: then GDN_DEV_TIMEOUT is set, and from
-// there on no wait of the block waits (its outputs are invalid), so that all its warps reach the
-// end.
+// Wait for a phase of a barrier, about a second at most: then GDN_DEV_TIMEOUT is set, and the
+// warps of the block leave after their next wait (its outputs are invalid).
 __device__ __forceinline__ void wait_phase(uint32_t bar, uint32_t parity, volatile int *abort, int32_t *status)
 {
     if (sm100::mbar_try_wait(bar, parity)) return;
@@ -247,6 +251,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     __shared__ Desc s_desc[kStages];
     __shared__ uint32_t s_valid[kStages][TILE / 32];
     __shared__ float4 s_stat[2][32];
+    __shared__ __align__(8) uint64_t s_meet;    // of the warps that compute
     __shared__ volatile int s_abort;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -264,34 +269,37 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             sm100::mbar_init(full0 + 8 * s, C::FETCH);
             sm100::mbar_init(empty0 + 8 * s, kConsumers / 32);
         }
+        sm100::mbar_init(smem_u32(&s_meet), kConsumers / 32);
         sm100::fence_mbar_init();
         sm100::prefetch_tmap(&kmap);
         sm100::prefetch_tmap(&vmap);
         if (!by_unit && in_range(c, 1, n_splits, a.dev_status)) splits[c].c1 = -1;
     }
 
-    // ---- this block's run of tiles
-    int64_t S = 0, incl0;      // tiles of the batch, a unit of each request; up to this thread's
-    const int nt0 = tid < a.B ? tiles_of<TILE>(a, row_info(a, tid, c == 0).len, box) : 0;
+    // ---- this block's run of places
+    int64_t S = 0, incl0;      // of the batch, a unit of each request; up to this thread's
+    const int nt0 = tid < a.B ? places_of<TILE>(a, row_info(a, tid, c == 0).len, box) : 0;
     {
         int64_t mine = nt0;
         for (int b = tid + kThreads; b < a.B; b += kThreads)
-            mine += tiles_of<TILE>(a, row_info(a, b, c == 0).len, box);
+            mine += places_of<TILE>(a, row_info(a, b, c == 0).len, box);
         incl0 = block_scan(mine, s_sum, &S);
     }
     const Deal deal(S * U, G);
     const int64_t t0 = deal.first(c);
-    const int n_tiles = deal.count(c);
+    const int n_places = deal.count(c);
 
-    // the request, unit and tile where it begins
-    if (n_tiles > 0) {
+    // the request, unit and place where it begins
+    if (tid == 0) s_found[2] = 0;
+    __syncthreads();
+    if (n_places > 0) {
         int64_t before = 0;
         for (int b0 = 0; b0 < a.B; b0 += kThreads) {
             const int b = b0 + tid;
             int nt = nt0;
             int64_t incl = incl0, all = S;
             if (a.B > kThreads) {       // the sum above was over more than a request a thread
-                nt = b < a.B ? tiles_of<TILE>(a, row_info(a, b, false).len, box) : 0;
+                nt = b < a.B ? places_of<TILE>(a, row_info(a, b, false).len, box) : 0;
                 incl = before + block_scan(nt, s_sum, &all);
             }
             if (nt > 0 && t0 >= (incl - nt) * U && t0 < incl * U) {
@@ -305,19 +313,29 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         }
     }
     __syncthreads();
+    // a run that ends before the first tile of the unit it begins in has none
+    const bool idle = n_places == 0 || n_places <= kUnitCost - s_found[2];
 
     if (warp >= kConsumers / 32) {
         // ================================================================ the warps that fetch
         registers_down<kFetchRegs>();
         const int fw = warp - kConsumers / 32;
-        if (n_tiles == 0 || fw >= C::FETCH) return;
+        if (idle || fw >= C::FETCH) return;
         int cb = s_found[0], win = cb;     // request; lane i knows about request win + i
         RowInfo mine = cb + lane < a.B ? row_info(a, cb + lane, false) : RowInfo{-1, 0};
         int len = __shfl_sync(0xffffffffu, mine.len, 0), slot = __shfl_sync(0xffffffffu, mine.slot, 0);
-        int cnt = tiles_of<TILE>(a, len, box);
-        int cu = s_found[1], ct = s_found[2];
-        for (int i = 0; i < n_tiles; ++i) {
-            const int st = i % kStages;
+        int cnt = places_of<TILE>(a, len, box);
+        int cu = s_found[1], cp = s_found[2];
+        int64_t place = t0;
+        int i = 0;
+        for (bool more = true; more; ++i) {
+            if (cp < kUnitCost) {               // the run holds a tile of the unit, or it had ended
+                place += kUnitCost - cp;
+                cp = kUnitCost;
+            }
+            const int st = i % kStages, ct = cp - kUnitCost;
+            const int left = (int)(t0 + n_places - place) - 1;      // places after this tile's
+            more = left > (cp + 1 == cnt ? kUnitCost : 0);
             const int base = first_tile(a, len, box) + ct * TILE, lo = first_seen(a, len);
             const int h = cu / RT;
             // a lane looks up a token of each 32
@@ -331,6 +349,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                 page[w] = j < len && in_range(pg, 1, kv.width, a.dev_status) ? __ldg(row + pg) : -1;
             }
             if (i >= kStages) wait_phase(empty0 + 8 * st, ((i / kStages) & 1) ^ 1, &s_abort, a.dev_status);
+            if (__any_sync(0xffffffffu, s_abort)) break;
             int boxes = 0;
 #pragma unroll
             for (int w = 0; w < C::FW; ++w) {
@@ -345,11 +364,12 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             if (lane == 0) {
                 if (fw == 0) {
                     Desc d;
-                    d.b = cb; d.u = cu; d.base = base; d.len = len; d.tile = ct; d.nt = cnt;
+                    d.b = cb; d.u = cu; d.base = base; d.len = len; d.tile = ct; d.nt = cnt - kUnitCost;
+                    d.last = !more; d.place = place;
                     s_desc[st] = d;
                 }
-                const uint32_t more = i == 0 && c == 0 && fw == 0 && gdn::test_stall_requested(a.dev_status) ? 16 : 0;
-                sm100::mbar_arrive_expect_tx(full0 + 8 * st, (uint32_t)(boxes * box * C::RB * 2) + more);
+                const uint32_t extra = i == 0 && c == 0 && fw == 0 && gdn::test_stall_requested(a.dev_status) ? 16 : 0;
+                sm100::mbar_arrive_expect_tx(full0 + 8 * st, (uint32_t)(boxes * box * C::RB * 2) + extra);
             }
             __syncwarp();
             const uint32_t ks = smem_u32(smem + st * 2 * kHalfStage), vs = ks + kHalfStage;
@@ -365,9 +385,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                         tma_load_4d(vs + k * TILE * 128 + to, &vmap, full0 + 8 * st, k * 128 / C::ESZ, at, h, page[w]);
                     }
                 }
-            // the next tile of the run (past the last one the cursor may stand anywhere)
-            if (++ct == cnt) {
-                ct = 0;
+            // the next place of the run (past the last one the cursor may stand anywhere)
+            ++place;
+            if (++cp == cnt) {
+                cp = 0;
                 if (++cu == U) {
                     cu = 0;
                     do {
@@ -378,15 +399,15 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                         }
                         len = __shfl_sync(0xffffffffu, mine.len, cb - win);
                         slot = __shfl_sync(0xffffffffu, mine.slot, cb - win);
-                        cnt = tiles_of<TILE>(a, len, box);
+                        cnt = places_of<TILE>(a, len, box);
                     } while (cnt == 0);
                 }
             }
         }
         if (s_abort) {      // no copy may land after the block is gone: a short wait for each stage
             const long long start = clock64();
-            for (int i = n_tiles > kStages ? n_tiles - kStages : 0; i < n_tiles; ++i)
-                while (!sm100::mbar_try_wait(full0 + 8 * (i % kStages), (i / kStages) & 1) &&
+            for (int k = i > kStages ? i - kStages : 0; k < i; ++k)
+                while (!sm100::mbar_try_wait(full0 + 8 * (k % kStages), (k / kStages) & 1) &&
                        clock64() - start < (1ll << 26)) {
                 }
         }
@@ -398,7 +419,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     // requests with nothing to see: zeros for a row of the cache, nothing (or zeros) for padding
     for (int b = c; b < a.B; b += G) {
         const RowInfo ri = row_info(a, b, false);
-        if (tiles_of<TILE>(a, ri.len, box) > 0) continue;
+        if (places_of<TILE>(a, ri.len, box) > 0) continue;
         if (by_unit)
             for (int u = tid; u < U; u += kConsumers)
                 if (in_range((int64_t)b * U + u, 1, n_splits, a.dev_status))
@@ -413,6 +434,17 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             for (int64_t i = tid; i < rows; i += kConsumers) a.lse[b * rows + i] = -INFINITY;
     }
 
+    if (idle) return;
+
+    const uint32_t meet = smem_u32(&s_meet);
+    uint32_t met = 0;       // parity of the next meeting
+    // all four warps are here (or, after a timeout, need not be)
+    auto meet_all = [&]() {
+        __syncwarp();
+        if (lane == 0) sm100::mbar_arrive(meet);
+        wait_phase(meet, met, &s_abort, a.dev_status);
+        met ^= 1;
+    };
     const int tq = lane & 3, lr = lane >> 2;
     const int wr = warp % WR, wd = (warp / WR) % C::WD, wt = warp / (WR * C::WD);
     // ---- the run
@@ -423,9 +455,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     int hi[E], lo[E];                       // a row sees lo < j <= hi
     int seg_tile = 0;                       // where the unit's part in this block began
 #pragma unroll 1
-    for (int i = 0; i < n_tiles; ++i) {
+    for (int i = 0;; ++i) {
         const int st = i % kStages;
         wait_phase(full0 + 8 * st, (i / kStages) & 1, &s_abort, a.dev_status);
+        if (__any_sync(0xffffffffu, s_abort)) break;
         const Desc d = s_desc[st];
         const int h = d.u / RT, rt = d.u - h * RT;
 
@@ -706,7 +739,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         __syncwarp();
         if (lane == 0) sm100::mbar_arrive(empty0 + 8 * st);
 
-        if (d.tile == d.nt - 1 || i == n_tiles - 1) {   // the unit, or its part here, is done
+        if (d.tile == d.nt - 1 || d.last) {   // the unit, or its part here, is done
 #pragma unroll
             for (int e = 0; e < E; ++e) {
                 l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
@@ -738,7 +771,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                                 buf[k * 32] = make_float4(o[2 * k][2 * e], o[2 * k][2 * e + 1],
                                                           o[2 * k + 1][2 * e], o[2 * k + 1][2 * e + 1]);
                     }
-                    sm100::named_sync(1, kConsumers);
+                    meet_all();
                     if (wt < half) {
                         if (e == 0) {
                             const float4 y = s_stat[warp % (half * WR * C::WD)][lane];
@@ -762,9 +795,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                                 o[2 * k + 1][2 * e + 1] = o[2 * k + 1][2 * e + 1] * f0[e] + y.w * f1[e];
                             }
                     }
-                    sm100::named_sync(1, kConsumers);
+                    meet_all();
                 }
             }
+            if (__any_sync(0xffffffffu, s_abort)) break;
             const bool whole = seg_tile == 0 && d.tile == d.nt - 1;
             if (wt == 0) {
 #pragma unroll
@@ -800,7 +834,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             // the block where a unit begins says who holds its parts
             if (tid == 0 && seg_tile == 0) {
                 const int64_t unit = (int64_t)d.b * U + d.u;
-                const int64_t end = t0 + i + (d.nt - 1 - d.tile);   // the unit's last tile
+                const int64_t end = d.place + (d.nt - 1 - d.tile);   // the unit's last tile
                 const int last = deal.owner(end);
                 const int64_t at = by_unit ? unit : c;
                 if ((by_unit || !whole) && in_range(at, 1, n_splits, a.dev_status)) {
@@ -810,6 +844,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                 }
             }
         }
+        if (d.last) break;
     }
 }
 
