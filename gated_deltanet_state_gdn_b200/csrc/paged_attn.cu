@@ -161,14 +161,26 @@ __device__ __forceinline__ int places_of(const GdnAttnArgs &a, int len, int box)
     return len > first_seen(a, len) ? kUnitCost + (len - first_tile(a, len, box) + TILE - 1) / TILE : 0;
 }
 
-// inclusive prefix sum over the block's threads; *total is the same in all
-__device__ __forceinline__ int64_t block_scan(int64_t x, int64_t *s, int64_t *total)
+// inclusive prefix sum over the block's threads; *total is the same in all.  With
+// `small` the values are of one request each, at most 2^25 + kUnitCost, and a warp's sum fits 32
+// bits.
+__device__ __forceinline__ int64_t block_scan(int64_t x, bool small, int64_t *s, int64_t *total)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (small) {
+        int y = (int)x;
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
-        if (lane >= d) x += y;
+        for (int d = 1; d < 32; d <<= 1) {
+            const int z = __shfl_up_sync(0xffffffffu, y, d);
+            if (lane >= d) y += z;
+        }
+        x = y;
+    } else {
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t z = __shfl_up_sync(0xffffffffu, x, d);
+            if (lane >= d) x += z;
+        }
     }
     if (lane == 31) s[warp] = x;
     __syncthreads();
@@ -283,15 +295,13 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         int64_t mine = nt0;
         for (int b = tid + kThreads; b < a.B; b += kThreads)
             mine += places_of<TILE>(a, row_info(a, b, c == 0).len, box);
-        incl0 = block_scan(mine, s_sum, &S);
+        incl0 = block_scan(mine, a.B <= kThreads, s_sum, &S);
     }
     const Deal deal(S * U, G);
     const int64_t t0 = deal.first(c);
     const int n_places = deal.count(c);
 
     // the request, unit and place where it begins
-    if (tid == 0) s_found[2] = 0;
-    __syncthreads();
     if (n_places > 0) {
         int64_t before = 0;
         for (int b0 = 0; b0 < a.B; b0 += kThreads) {
@@ -300,7 +310,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             int64_t incl = incl0, all = S;
             if (a.B > kThreads) {       // the sum above was over more than a request a thread
                 nt = b < a.B ? places_of<TILE>(a, row_info(a, b, false).len, box) : 0;
-                incl = before + block_scan(nt, s_sum, &all);
+                incl = before + block_scan(nt, true, s_sum, &all);
             }
             if (nt > 0 && t0 >= (incl - nt) * U && t0 < incl * U) {
                 const int64_t past = t0 - (incl - nt) * U;
@@ -848,23 +858,24 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     }
 }
 
-// Joins the rows of units that several blocks worked on, `per` rows a block.  Up to kFew parts of
-// a row are joined by one warp, eight rows side by side; more by the whole block, row by row,
-// sixteen groups of threads taking every sixteenth part.
+// Joins the rows of units that several blocks worked on.  `per` == kJoinRows (many units): eight
+// rows a block, one warp a row of up to kFew parts.  Otherwise, and for rows of more parts, the
+// whole block takes a row, 64 dimensions at a time, sixteen groups of threads every sixteenth
+// part; with `per` == 1 a block has one row and 64 dimensions.
+constexpr int kJoin = 256;
 constexpr int kJoinGroups = 16;
 constexpr int kMaxBlocks = 1024;
 constexpr int kFew = 8;
-constexpr int kJoinRows = 8;
+constexpr int kJoinRows = kJoin / 32;
 
 template <int DP>
-__global__ void __launch_bounds__(kJoinGroups *DP / 4)
+__global__ void __launch_bounds__(kJoin)
 paged_attn_join_kernel(const GdnAttnArgs a, const int RT, const int RMAX, const int per,
                        const Split *const splits, const float2 *const part_ml, const float *const part_o)
 {
-    constexpr int kJoin = kJoinGroups * DP / 4;
     __shared__ float s_w[kMaxBlocks];                   // weights of the parts
     __shared__ float s_red[2][kJoin / 32];
-    __shared__ float4 s_o[kJoinGroups][DP / 4];
+    __shared__ float4 s_o[kJoinGroups][16];
     wait_primary();
     const Split sp = splits[blockIdx.x];
     if (sp.c1 < 0) return;
@@ -888,118 +899,128 @@ paged_attn_join_kernel(const GdnAttnArgs a, const int RT, const int RMAX, const 
     const int64_t all_rows = (int64_t)a.B * a.T * a.Hq;
 
     if (per == kJoinRows && np <= kFew) {
-        for (int rl = blockIdx.y * per + warp; rl < min(rows, (int)(blockIdx.y + 1) * per); rl += kJoin / 32) {
-            float2 ml = make_float2(-INFINITY, 0.f);
-            if (lane < np) ml = __ldcg(part_ml + at(lane, rl));
-            float top = ml.x;
+        const int rl = blockIdx.y * per + warp;
+        if (rl >= rows) return;
+        constexpr int PER = (DP + 127) / 128;           // float4 a thread
+        float4 y[PER][kFew];
 #pragma unroll
-            for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-            const float ms = top == -INFINITY ? 0.f : top;
-            const float w = ex2_approx(ml.x - ms);
-            const float sum = gdn::warp_sum(ml.y * w);
-            const int64_t row = place(rl);
-            const bool ok = in_range(row, 1, all_rows, a.dev_status);
-            for (int d0 = 0; d0 < D; d0 += 128) {
-                const int d = d0 + 4 * lane;
-                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < kFew; ++k)
 #pragma unroll
-                for (int k = 0; k < kFew; ++k) {
-                    const float wk = __shfl_sync(0xffffffffu, w, k);
-                    if (k < np && d < D) {
-                        const float4 y = __ldcg(reinterpret_cast<const float4 *>(part_o + at(k, rl) * DP + d));
-                        acc.x += wk * y.x;
-                        acc.y += wk * y.y;
-                        acc.z += wk * y.z;
-                        acc.w += wk * y.w;
-                    }
+            for (int e = 0; e < PER; ++e)
+                y[e][k] = k < np && (e * 32 + lane) * 4 < DP
+                              ? __ldcg(reinterpret_cast<const float4 *>(part_o + at(k, rl) * DP) + e * 32 + lane)
+                              : make_float4(0.f, 0.f, 0.f, 0.f);
+        float2 ml = make_float2(-INFINITY, 0.f);
+        if (lane < np) ml = __ldcg(part_ml + at(lane, rl));
+        float top = ml.x;
+#pragma unroll
+        for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+        const float ms = top == -INFINITY ? 0.f : top;
+        const float w = ex2_approx(ml.x - ms);
+        const float sum = gdn::warp_sum(ml.y * w);
+        const int64_t row = place(rl);
+        const bool ok = in_range(row, 1, all_rows, a.dev_status);
+#pragma unroll
+        for (int e = 0; e < PER; ++e) {
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < kFew; ++k) {
+                const float wk = __shfl_sync(0xffffffffu, w, k);
+                if (k < np) {
+                    acc.x += wk * y[e][k].x;
+                    acc.y += wk * y[e][k].y;
+                    acc.z += wk * y[e][k].z;
+                    acc.w += wk * y[e][k].w;
                 }
-                if (ok && d < D) store(row, d, acc, sum);
             }
-            if (ok && a.lse && lane == 0) a.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+            const int d = (e * 32 + lane) * 4;
+            if (ok && d < D) store(row, d, acc, sum);
         }
+        if (ok && a.lse && lane == 0) a.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
         return;
     }
 
-    const int grp = tid / (DP / 4), d4 = tid % (DP / 4);
-    constexpr int kAhead = 4;
+    const int grp = tid / 16, d4 = tid % 16;
+    constexpr int kAhead = 10;
     constexpr int kMl = kMaxBlocks / kJoin;             // np <= kMaxBlocks
-    for (int rl = blockIdx.y * per; rl < min(rows, (int)(blockIdx.y + 1) * per); ++rl) {
-        // the values come first: they do not depend on the weights
-        float4 y[kAhead];
-        auto fetch = [&](int k0) {
+    for (int rl = blockIdx.y * per; rl < min(rows, (int)(blockIdx.y + 1) * per); ++rl)
+        for (int d0 = blockIdx.z * 64; d0 < D; d0 += 64 * gridDim.z) {
+            // the values come first: they do not depend on the weights
+            float4 y[kAhead];
+            auto fetch = [&](int k0) {
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                const int k = k0 + u * kJoinGroups;
-                y[u] = k < np ? __ldcg(reinterpret_cast<const float4 *>(part_o + at(k, rl) * DP) + d4)
-                              : make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int u = 0; u < kAhead; ++u) {
+                    const int k = k0 + u * kJoinGroups;
+                    y[u] = k < np ? __ldcg(reinterpret_cast<const float4 *>(part_o + at(k, rl) * DP + d0) + d4)
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+                }
+            };
+            fetch(grp);
+            float top = -INFINITY;
+            float2 ml[kMl];
+#pragma unroll
+            for (int u = 0; u < kMl; ++u) {
+                const int k = tid + u * kJoin;
+                ml[u] = k < np ? __ldcg(part_ml + at(k, rl)) : make_float2(-INFINITY, 0.f);
+                top = fmaxf(top, ml[u].x);
             }
-        };
-        fetch(grp);
-        float top = -INFINITY;
-        float2 ml[kMl];
 #pragma unroll
-        for (int u = 0; u < kMl; ++u) {
-            const int k = tid + u * kJoin;
-            ml[u] = k < np ? __ldcg(part_ml + at(k, rl)) : make_float2(-INFINITY, 0.f);
-            top = fmaxf(top, ml[u].x);
-        }
+            for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+            if (lane == 0) s_red[0][warp] = top;
+            __syncthreads();
 #pragma unroll
-        for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-        if (lane == 0) s_red[0][warp] = top;
-        __syncthreads();
+            for (int w = 0; w < kJoin / 32; ++w) top = fmaxf(top, s_red[0][w]);
+            const float ms = top == -INFINITY ? 0.f : top;
+            float sum = 0.f;
 #pragma unroll
-        for (int w = 0; w < kJoin / 32; ++w) top = fmaxf(top, s_red[0][w]);
-        const float ms = top == -INFINITY ? 0.f : top;
-        float sum = 0.f;
-#pragma unroll
-        for (int u = 0; u < kMl; ++u) {
-            const int k = tid + u * kJoin;
-            const float w = ex2_approx(ml[u].x - ms);
-            if (k < np) {
-                s_w[k] = w;
-                sum += ml[u].y * w;
+            for (int u = 0; u < kMl; ++u) {
+                const int k = tid + u * kJoin;
+                const float w = ex2_approx(ml[u].x - ms);
+                if (k < np) {
+                    s_w[k] = w;
+                    sum += ml[u].y * w;
+                }
             }
-        }
-        sum = gdn::warp_sum(sum);
-        if (lane == 0) s_red[1][warp] = sum;
-        __syncthreads();
-        sum = 0.f;
+            sum = gdn::warp_sum(sum);
+            if (lane == 0) s_red[1][warp] = sum;
+            __syncthreads();
+            sum = 0.f;
 #pragma unroll
-        for (int w = 0; w < kJoin / 32; ++w) sum += s_red[1][w];
+            for (int w = 0; w < kJoin / 32; ++w) sum += s_red[1][w];
 
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int k0 = grp; k0 < np; k0 += kAhead * kJoinGroups) {
-            if (k0 != grp) fetch(k0);
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k0 = grp; k0 < np; k0 += kAhead * kJoinGroups) {
+                if (k0 != grp) fetch(k0);
 #pragma unroll
-            for (int u = 0; u < kAhead; ++u) {
-                const int k = k0 + u * kJoinGroups;
-                if (k >= np) break;
-                const float w = s_w[k];
-                acc.x += w * y[u].x;
-                acc.y += w * y[u].y;
-                acc.z += w * y[u].z;
-                acc.w += w * y[u].w;
+                for (int u = 0; u < kAhead; ++u) {
+                    const int k = k0 + u * kJoinGroups;
+                    if (k >= np) break;
+                    const float w = s_w[k];
+                    acc.x += w * y[u].x;
+                    acc.y += w * y[u].y;
+                    acc.z += w * y[u].z;
+                    acc.w += w * y[u].w;
+                }
             }
-        }
-        s_o[grp][d4] = acc;
-        __syncthreads();
-        const int64_t row = place(rl);
-        const bool ok = in_range(row, 1, all_rows, a.dev_status);
-        if (ok && tid < D / 4) {
-            acc = s_o[0][tid];
+            s_o[grp][d4] = acc;
+            __syncthreads();
+            const int64_t row = place(rl);
+            const bool ok = in_range(row, 1, all_rows, a.dev_status);
+            if (ok && tid < 16 && d0 + 4 * tid < D) {
+                acc = s_o[0][tid];
 #pragma unroll
-            for (int g = 1; g < kJoinGroups; ++g) {
-                const float4 z = s_o[g][tid];
-                acc.x += z.x;
-                acc.y += z.y;
-                acc.z += z.z;
-                acc.w += z.w;
+                for (int g = 1; g < kJoinGroups; ++g) {
+                    const float4 z = s_o[g][tid];
+                    acc.x += z.x;
+                    acc.y += z.y;
+                    acc.z += z.z;
+                    acc.w += z.w;
+                }
+                store(row, d0 + 4 * tid, acc, sum);
             }
-            store(row, 4 * tid, acc, sum);
+            if (ok && a.lse && tid == 0 && d0 == 0) a.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+            __syncthreads();        // the shared arrays are used again
         }
-        if (ok && a.lse && tid == 0) a.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
-        __syncthreads();        // the shared arrays are used again
-    }
 }
 
 // ------------------------------------------------------------------ host
@@ -1097,9 +1118,9 @@ cudaError_t launch(const GdnAttnArgs &a, cudaStream_t stream)
     if (e == cudaSuccess) e = encode(&vmap, kv.v, kv, C::ESZ, C::RB, box);
     if (e != cudaSuccess) return e;
     const Layout y = layout(a.B, a.T, a.Hq, kv.heads, DP, max_blocks());
-    // no more blocks than there can be tiles
+    // no more blocks than there can be places in the deal
     const int64_t cap = (int64_t)kv.width * kv.page_size;
-    const double tiles = (double)a.B * kv.heads * y.RT * (double)((cap + C::TILE - 1) / C::TILE + 1);
+    const double tiles = (double)a.B * kv.heads * y.RT * (double)((cap + C::TILE - 1) / C::TILE + 1 + kUnitCost);
     const int blocks = tiles < max_blocks() ? (int)tiles : max_blocks();
     unsigned char *const ws = static_cast<unsigned char *>(a.workspace);
     Split *const splits = reinterpret_cast<Split *>(ws);
@@ -1111,12 +1132,12 @@ cudaError_t launch(const GdnAttnArgs &a, cudaStream_t stream)
                                                                            n_splits, ml, o);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    // Few units: many parts each, a block a row.  Many: two or three parts each as a rule, a warp a
-    // row and eight rows a block.
+    // many units have two or three parts each as a rule, few many
     const int rows = std::min(y.RMAX, a.T * (a.Hq / kv.heads));
     const int per = units * kFew >= blocks ? kJoinRows : 1;
-    return launch_dependent(paged_attn_join_kernel<DP>, dim3(n_splits, (rows + per - 1) / per),
-                            dim3(kJoinGroups * DP / 4), 0, stream, a, y.RT, y.RMAX, per, splits, ml, o);
+    return launch_dependent(paged_attn_join_kernel<DP>,
+                            dim3(n_splits, (rows + per - 1) / per, per == 1 ? DP / 64 : 1), dim3(kJoin), 0,
+                            stream, a, y.RT, y.RMAX, per, splits, ml, o);
 }
 
 // A box starts on 128 bytes of shared memory: 64-byte rows need an even number of tokens, so
