@@ -1,9 +1,11 @@
 // kv_append.cu -- new keys and values to the pages of their positions.
 //
 // HBM-bound: every value is read once and written once, 4 bytes a value in 16 bits and 3 into 8.
-// A block takes a few tokens, all their heads, keys and values.  Its first loads are issued
-// before the tokens' places are known (a chain of four dependent loads: offsets, slot, length,
-// page), so the two latencies overlap; then each thread stores what it holds.
+// Where a token goes hangs on a chain of four dependent loads (offsets, slot, length, page), so a
+// block has a warp for it that works a chunk of tokens ahead of the eight that copy; blocks stay
+// and take every so-many-th chunk of equal size.  A copying thread keeps one column (keys or values, head, 8
+// dimensions) and walks the tokens, so that nothing is divided in the loop; its loads are issued
+// before it waits for the places.
 #include "cache.cuh"
 
 namespace gdn_append {
@@ -11,12 +13,25 @@ namespace gdn_append {
 using namespace gdn_cache;
 using gdn::in_range;
 
-constexpr int kThreads = 256;
-constexpr int kHold = 4;         // 16-byte pieces a thread holds at a time
-constexpr int kMaxTokens = 32;   // tokens a block
+constexpr int kThreads = 256;     // that copy
+constexpr int kHold = 4;          // 16-byte pieces a thread holds at a time
+constexpr int kMaxTokens = 32;    // of a chunk: a lane of the placing warp each
+constexpr int kBlocksSM = 4;
+constexpr int kOffsets = 1024;    // offsets that a block searches in shared memory
+
+// x / scale to nearest, for a quotient within +-1024 (past 448 every quotient is stored as 448, so
+// there the product with the reciprocal will do, infinities included).  With r the reciprocal
+// rounded to nearest, one step of the remainder from x r gives the rounded quotient (Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000 processor", 1990).
+__device__ __forceinline__ float quotient(float x, float scale, float r)
+{
+    const float q = x * r;
+    const float y = fmaf(fmaf(-q, scale, x), r, q);
+    return fabsf(q) < 1024.f ? y : q;
+}
 
 // eight 16-bit values -> eight e4m3 numbers of x / scale
-__device__ __forceinline__ uint2 quantise(const uint4 &w, bool bf16, float scale)
+__device__ __forceinline__ uint2 quantise(const uint4 &w, bool bf16, float scale, float r, bool plain)
 {
     const uint32_t in[4] = {w.x, w.y, w.z, w.w};
     uint32_t out[2] = {0u, 0u};
@@ -30,40 +45,41 @@ __device__ __forceinline__ uint2 quantise(const uint4 &w, bool bf16, float scale
             lo = __half2float(__ushort_as_half((unsigned short)(in[k] & 0xffffu)));
             hi = __half2float(__ushort_as_half((unsigned short)(in[k] >> 16)));
         }
+        const float2 y = plain ? make_float2(quotient(lo, scale, r), quotient(hi, scale, r))
+                               : make_float2(__fdiv_rn(lo, scale), __fdiv_rn(hi, scale));
         // one rounding to float32, then one to e4m3 (to nearest even; past 448, infinities too,
         // to the largest number; a NaN stays one)
-        const __nv_fp8x2_storage_t y = __nv_cvt_float2_to_fp8x2(
-            make_float2(__fdiv_rn(lo, scale), __fdiv_rn(hi, scale)), __NV_SATFINITE, __NV_E4M3);
-        out[k / 2] |= (uint32_t)y << (16 * (k & 1));
+        out[k / 2] |= (uint32_t)__nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3) << (16 * (k & 1));
     }
     return make_uint2(out[0], out[1]);
 }
 
-// where token n goes: element offset of its head 0 in the cache, or -1
-__device__ int64_t place(const GdnAppendArgs &a, int64_t n)
+// where token n goes: element offset of its head 0 in the cache, or -1; `offsets` are the row
+// offsets in global or shared memory
+__device__ int64_t place(const GdnAppendArgs &a, int64_t n, const int32_t *offsets)
 {
     const gdn_paged_cache &kv = a.cache;
     int b;
     int64_t end;
-    if (a.row_offsets) {
+    if (offsets) {
         // The request with s <= n < e; offsets ascend, so it is the last whose s is <= n (empty
         // requests before it end at or before n).
         int lo = 0, hi = a.B;        // offsets[lo] <= n < offsets[hi], were they sentinels
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if (__ldg(a.row_offsets + mid) <= n)
+            if (offsets[mid] <= n)
                 lo = mid;
             else
                 hi = mid;
         }
         b = lo;
-        if (n < __ldg(a.row_offsets + b)) return -1;    // ahead of the first request
-        end = __ldg(a.row_offsets + b + 1);
+        if (n < offsets[b]) return -1;    // ahead of the first request
+        end = offsets[b + 1];
         if (end > a.N) end = a.N;
-        if (n >= end) return -1;                        // behind the last one
+        if (n >= end) return -1;          // behind the last one
     } else {
-        const int64_t T = a.N / a.B;
-        b = (int)(n / T);
+        const int T = (int)(a.N / a.B);
+        b = (int)n / T;
         end = (int64_t)(b + 1) * T;
     }
     const int slot = a.slots ? __ldg(a.slots + b) : b;
@@ -90,64 +106,79 @@ __device__ int64_t place(const GdnAppendArgs &a, int64_t n)
 }
 
 template <bool E4M3>
-__global__ void __launch_bounds__(kThreads) kv_append_kernel(const GdnAppendArgs a, const int tokens)
+__global__ void __launch_bounds__(kThreads + 32, kBlocksSM)
+kv_append_kernel(const __grid_constant__ GdnAppendArgs a, const int tokens, const int64_t chunks)
 {
-    __shared__ int64_t s_at[kMaxTokens];
+    __shared__ int64_t s_at[2][kMaxTokens];
+    __shared__ int32_t s_offsets[kOffsets];
     const gdn_paged_cache &kv = a.cache;
     const int tid = threadIdx.x, D8 = kv.head_dim / 8, per_token = 2 * kv.heads * D8;
-    const int64_t n0 = (int64_t)blockIdx.x * tokens;
-    const int here = (int)(a.N - n0 < tokens ? a.N - n0 : tokens);
-    const int pieces = here * per_token;
+    auto size_of = [&](int64_t chunk) { return (int)min(a.N - chunk * tokens, (int64_t)tokens); };
+
+    if (tid >= kThreads) {
+        const int lane = tid - kThreads;
+        const bool staged = a.row_offsets && a.B < kOffsets;
+        if (staged)
+            for (int i = lane; i <= a.B; i += 32) s_offsets[i] = __ldg(a.row_offsets + i);
+        __syncwarp();
+        const int32_t *const offsets = staged ? s_offsets : a.row_offsets;
+        int buf = 0;
+        for (int64_t chunk = blockIdx.x; chunk < chunks; chunk += gridDim.x, buf ^= 1) {
+            // (the chunk before the last one has been copied: the others are past its meeting)
+            if (lane < size_of(chunk)) s_at[buf][lane] = place(a, chunk * tokens + lane, offsets);
+            __syncthreads();
+        }
+        return;
+    }
+
     const int64_t cache_n = (int64_t)(kv.num_pages - 1) * kv.page_stride +
                             (int64_t)(kv.page_size - 1) * kv.token_stride +
                             (int64_t)(kv.heads - 1) * kv.head_stride + kv.head_dim;
-
-    // piece i of the block: token, keys or values, head, 8 dimensions
-    struct Piece { int t, v, h, d; };
-    auto piece = [&](int i) {
-        Piece p;
-        p.t = i / per_token;
-        int r = i - p.t * per_token;
-        const int half = kv.heads * D8;
-        p.v = r >= half;
-        r -= p.v ? half : 0;
-        p.h = r / D8;
-        p.d = (r - p.h * D8) * 8;
-        return p;
-    };
-    bool placed = false;
-    for (int i0 = tid; i0 - tid < pieces; i0 += kThreads * kHold) {
-        uint4 w[kHold];
+    // tokens side by side in the block, and this thread's column
+    const int side = per_token < kThreads ? kThreads / per_token : 1;
+    const int t0 = per_token < kThreads ? tid / per_token : 0;
+    const int col0 = per_token < kThreads ? tid - t0 * per_token : tid;
+    int buf = 0;
+    for (int64_t chunk = blockIdx.x; chunk < chunks; chunk += gridDim.x, buf ^= 1) {
+        const int64_t n0 = chunk * tokens;
+        const int here = size_of(chunk);
+#pragma unroll 1
+        for (int c0 = 0; c0 < per_token; c0 += kThreads) {
+            const int col = c0 + col0;
+            const bool mine = col < per_token && t0 < side;
+            const int v = col >= kv.heads * D8, r = col - (v ? kv.heads * D8 : 0), h = r / D8, d = (r - h * D8) * 8;
+            const int64_t ts = v ? a.v_token_stride : a.k_token_stride;
+            const uint16_t *x = static_cast<const uint16_t *>(v ? a.v : a.k) + (n0 + t0) * ts +
+                                h * (v ? a.v_head_stride : a.k_head_stride) + d;
+            const int64_t off = h * kv.head_stride + d;
+            unsigned char *const y = static_cast<unsigned char *>(v ? kv.v : kv.k) + off * (E4M3 ? 1 : 2);
+            float scale = 1.f, inv = 1.f;
+            if (E4M3 && mine) {
+                const float *const sc = v ? kv.v_scale : kv.k_scale;
+                if (sc) scale = __ldg(sc + h);
+                inv = __frcp_rn(scale);
+            }
+            // (a scale whose reciprocal is no normal number is divided by)
+            const bool plain = fabsf(scale) > 0x1p-120f && fabsf(scale) < 0x1p120f;
+#pragma unroll 1
+            for (int i = t0; i - t0 < here; i += side * kHold) {
+                uint4 w[kHold];
 #pragma unroll
-        for (int k = 0; k < kHold; ++k) {
-            const int i = i0 + k * kThreads;
-            if (i >= pieces) continue;
-            const Piece p = piece(i);
-            const uint16_t *const x = static_cast<const uint16_t *>(p.v ? a.v : a.k);
-            const int64_t ts = p.v ? a.v_token_stride : a.k_token_stride;
-            const int64_t hs = p.v ? a.v_head_stride : a.k_head_stride;
-            w[k] = __ldcs(reinterpret_cast<const uint4 *>(x + (n0 + p.t) * ts + p.h * hs + p.d));
-        }
-        if (!placed) {
-            if (tid < here) s_at[tid] = place(a, n0 + tid);
-            __syncthreads();
-            placed = true;
-        }
+                for (int k = 0; k < kHold; ++k) {
+                    if (mine && i + k * side < here) w[k] = __ldcs(reinterpret_cast<const uint4 *>(x));
+                    x += side * ts;
+                }
+                if (c0 == 0 && i == t0) __syncthreads();        // the places are known
 #pragma unroll
-        for (int k = 0; k < kHold; ++k) {
-            const int i = i0 + k * kThreads;
-            if (i >= pieces) continue;
-            const Piece p = piece(i);
-            if (s_at[p.t] < 0) continue;
-            const int64_t to = s_at[p.t] + p.h * kv.head_stride + p.d;
-            if (!in_range(to, 8, cache_n, a.dev_status)) continue;
-            if constexpr (E4M3) {
-                const float *const sc = p.v ? kv.v_scale : kv.k_scale;
-                const float s = sc ? __ldg(sc + p.h) : 1.f;
-                *reinterpret_cast<uint2 *>(static_cast<unsigned char *>(p.v ? kv.v : kv.k) + to) =
-                    quantise(w[k], a.bf16 != 0, s);
-            } else {
-                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.v ? kv.v : kv.k) + to) = w[k];
+                for (int k = 0; k < kHold; ++k) {
+                    const int t = i + k * side;
+                    const int64_t at = mine && t < here ? s_at[buf][t] : -1;
+                    if (at < 0 || !in_range(at + off, 8, cache_n, a.dev_status)) continue;
+                    if constexpr (E4M3)
+                        *reinterpret_cast<uint2 *>(y + at) = quantise(w[k], a.bf16 != 0, scale, inv, plain);
+                    else
+                        *reinterpret_cast<uint4 *>(y + 2 * at) = w[k];
+                }
             }
         }
     }
@@ -158,17 +189,15 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const GdnAppendArgs
 cudaError_t launch_kv_append(const GdnAppendArgs &a, cudaStream_t stream)
 {
     using namespace gdn_append;
-    // tokens a block: up to what its threads hold at once, fewer when that leaves SMs idle
-    const int64_t per_token = 2 * (int64_t)a.cache.heads * (a.cache.head_dim / 8);
-    int64_t tokens = kThreads * kHold / per_token;
-    const int64_t spread = a.N / (4 * gdn_cache::sm_count() + 1);
-    if (tokens > spread) tokens = spread;
-    if (tokens > kMaxTokens) tokens = kMaxTokens;
-    if (tokens < 1) tokens = 1;
-    const int64_t blocks = (a.N + tokens - 1) / tokens;
+    // equal chunks of at most kMaxTokens, in as few rounds of the resident blocks as that takes
+    const int64_t resident = (int64_t)kBlocksSM * gdn_cache::sm_count();
+    const int64_t rounds = (a.N + resident * kMaxTokens - 1) / (resident * kMaxTokens);
+    const int64_t tokens = (a.N + resident * rounds - 1) / (resident * rounds);
+    const int64_t chunks = (a.N + tokens - 1) / tokens;
+    const unsigned blocks = (unsigned)(chunks < resident ? chunks : resident);
     if (a.cache.dtype == GDN_E4M3)
-        kv_append_kernel<true><<<(unsigned)blocks, kThreads, 0, stream>>>(a, (int)tokens);
+        kv_append_kernel<true><<<blocks, kThreads + 32, 0, stream>>>(a, (int)tokens, chunks);
     else
-        kv_append_kernel<false><<<(unsigned)blocks, kThreads, 0, stream>>>(a, (int)tokens);
+        kv_append_kernel<false><<<blocks, kThreads + 32, 0, stream>>>(a, (int)tokens, chunks);
     return cudaGetLastError();
 }
