@@ -2,8 +2,8 @@
 // rows, with the copies of pages and states that follow.
 //
 // The tables are integers of a few megabytes at most; a call's time is the latency of its
-// dependent steps.  Resize and compact run them in one cluster of eight blocks, whose barrier
-// orders the steps (about a microsecond each where a launch a step would cost two to three).
+// dependent steps.  Resize and compact run them in one cluster of blocks, whose barrier orders the
+// steps (about half a microsecond each where a launch a step would cost two to three).
 // The copies are HBM-bound (each byte read once and written once) and run in a second kernel
 // over the whole GPU, brought up while the first one drains.  Everything is decided by scans in
 // the order of the lists and of the page numbers, so a call has one result; atomics only count
@@ -18,10 +18,11 @@ namespace cg = cooperative_groups;
 using namespace gdn_cache;
 using gdn::in_range;
 
-constexpr int kCluster = 8;
-constexpr int kThreads = 1024;          // of a planning block
-constexpr int kWarps = kCluster * kThreads / 32;
-constexpr int kChunk = 128;             // table entries a warp takes at a time
+constexpr int kCluster = 16;            // planning blocks at most
+constexpr int kThreads = 1024;          // of one
+constexpr int kChunk = 256;             // table entries a warp takes at a time
+constexpr int kPer = 16;                // pages a thread takes at a time
+constexpr int kNear = 1024;             // listed rows whose plan is kept in shared memory
 constexpr int kCopyThreads = 256;
 constexpr int kCopyBytes = 16384;       // of a row a block copies at a time
 constexpr int kMaxPools = 96;           // a launch (a kernel's arguments hold 4 KB)
@@ -38,7 +39,7 @@ struct Pools {
 
 struct alignas(16) Row {                // what resize does to a listed row
     int row, had, want, first;          // pages before and after; first new page's place
-    int len, copied, last, pad;         // new length; a shared page is replaced; that page
+    int len, copied, last, need;        // new length; a shared page is replaced, that page; new pages
 };
 
 __device__ __forceinline__ void tell(int32_t *status, int bit)
@@ -75,6 +76,31 @@ __device__ __forceinline__ int block_scan(int x, int *s_warp, int *total)
     *total = __shfl_sync(0xffffffffu, wi, 31);
     __syncthreads();                    // s_warp is used again
     return before + incl - x;
+}
+
+// Bit k: page p + k (< end) is used (free).  Whole vectors where the counts are aligned.
+__device__ __forceinline__ uint32_t used_pages(const int32_t *ref, int p, int end, bool vec, uint32_t *in)
+{
+    uint32_t used = 0, there = 0;
+    if (vec && p + kPer <= end) {
+        int4 v[kPer / 4];
+#pragma unroll
+        for (int k = 0; k < kPer / 4; ++k) v[k] = __ldcg(reinterpret_cast<const int4 *>(ref + p) + k);
+#pragma unroll
+        for (int k = 0; k < kPer / 4; ++k)
+            used |= ((uint32_t)(v[k].x > 0) | (uint32_t)(v[k].y > 0) << 1 | (uint32_t)(v[k].z > 0) << 2 |
+                     (uint32_t)(v[k].w > 0) << 3) << (4 * k);
+        there = (1u << kPer) - 1;
+    } else {
+#pragma unroll
+        for (int k = 0; k < kPer; ++k)
+            if (p + k < end) {
+                used |= (uint32_t)(__ldcg(ref + p + k) > 0) << k;
+                there |= 1u << k;
+            }
+    }
+    *in = there;
+    return used;
 }
 
 // copy piece `item` of row src to row dst
@@ -114,40 +140,44 @@ __device__ __forceinline__ void copy_piece(const Pools &ps, int item, int64_t sr
     }
 }
 
-// The copies that a plan wrote down: pairs[k] = (src, dst), disjoint.  With a table, its entries
-// are first renamed by `map` (compact).
-__global__ void __launch_bounds__(kCopyThreads)
-copy_pairs_kernel(const __grid_constant__ Pools ps, const int2 *pairs, const int *count,
-                  const int num_rows, const gdn_page_table t, const int32_t *map, int32_t *status)
+// Table entries renamed by `map` (compact): a warp takes a row of the table at a time.
+__device__ __noinline__ void rename_rows(const gdn_page_table &t, const int32_t *map, int32_t *status)
 {
-    wait_primary();
-    const int n = *count;
-    if (map) {
-        const int64_t words = (int64_t)t.rows * t.width;
-        for (int64_t i = (int64_t)blockIdx.x * kCopyThreads + threadIdx.x; i < words;
-             i += (int64_t)gridDim.x * kCopyThreads) {
-            const int s = (int)(i / t.width), j = (int)(i - (int64_t)s * t.width);
-            const int len = __ldg(t.seq_lens + s);
-            if (!length_ok(t, len)) {
-                if (j == 0) tell(status, GDN_DEV_BAD_LENGTH);
-                continue;
-            }
-            if (j >= pages_of(len, t.page_size)) continue;
-            int32_t *const e = t.block_table + s * t.table_stride + j;
-            const int id = *e;
+    const int lane = threadIdx.x & 31;
+    for (int s = blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5); s < t.rows;
+         s += gridDim.x * (kCopyThreads / 32)) {
+        const int len = __ldg(t.seq_lens + s);
+        if (!length_ok(t, len)) {
+            if (lane == 0) tell(status, GDN_DEV_BAD_LENGTH);
+            continue;
+        }
+        int32_t *const e = t.block_table + s * t.table_stride;
+        const int had = pages_of(len, t.page_size);
+        for (int j = lane; j < had; j += 32) {
+            const int id = e[j];
             const int to = (uint32_t)id < (uint32_t)t.num_pages ? __ldcg(map + id) : -1;
             if (to < 0)
                 tell(status, GDN_DEV_BAD_PAGE);
             else if (to != id)
-                *e = to;
+                e[j] = to;
         }
     }
-    const int64_t items = (int64_t)n * ps.pieces;
+}
+
+// The copies that a plan wrote down: pairs[k] = (src, dst), disjoint.  With a map, the table's
+// entries are renamed too.
+__global__ void __launch_bounds__(kCopyThreads)
+copy_pairs_kernel(const __grid_constant__ Pools ps, const int2 *pairs, const int *count,
+                  const int num_rows, const __grid_constant__ gdn_page_table t, const int32_t *map, int32_t *status)
+{
+    wait_primary();
+    const int64_t items = (int64_t)*count * ps.pieces;
     for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
         const int2 p = pairs[i / ps.pieces];
         if (in_range(p.x, 1, num_rows, status) && in_range(p.y, 1, num_rows, status))
             copy_piece(ps, (int)(i % ps.pieces), p.x, p.y);
     }
+    if (map) rename_rows(t, map, status);
 }
 
 // ------------------------------------------------------------------ resize
@@ -159,32 +189,45 @@ struct ResizeWork {
     int *free_list;
 };
 
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
-resize_kernel(const gdn_page_table t, const int32_t *row_list, const int32_t *new_lens, const int n,
-              const ResizeWork ws, int32_t *status)
+__global__ void __launch_bounds__(kThreads, 1)
+resize_kernel(const __grid_constant__ gdn_page_table t, const int32_t *row_list, const int32_t *new_lens,
+              const int n, const ResizeWork ws, int32_t *status)
 {
     cg::cluster_group cluster = cg::this_cluster();
-    const int rank = (int)cluster.block_rank(), tid = threadIdx.x, lane = tid & 31;
-    const int gw = (tid >> 5) * kCluster + rank;       // warp of the cluster
-    __shared__ int s_list[kThreads];
+    const int blocks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warps = blocks * (kThreads / 32), gw = (tid >> 5) * blocks + rank;    // of the cluster
+    __shared__ __align__(16) int s_list[kThreads];
     __shared__ int s_warp[32];
     __shared__ int s_most[2];
     __shared__ int s_free;
-    Row *const rows = ws.rows + (int64_t)rank * n;
+    __shared__ Row s_rows[kNear];
+    Row *const rows = n <= kNear ? s_rows : ws.rows + (int64_t)rank * n;
     launch_dependents();
+    // the steps' order: among the blocks, or the threads of the only one
+    auto meet = [&]() {
+        if (blocks > 1) cluster.sync(); else __syncthreads();
+    };
 
     // 1. what is asked of each row (every block works it out for itself)
     if (tid == 0) s_most[0] = s_most[1] = 0;
     for (int i0 = 0; i0 < n; i0 += kThreads) {
         const int i = i0 + tid;
         const int r = i < n ? __ldg(row_list + i) : -1;
+        const bool there = r >= 0 && r < t.rows;
+        const int old = there ? __ldcg(t.seq_lens + r) : 0, len = i < n ? __ldg(new_lens + i) : 0;
         int twice = 0;
         for (int k0 = 0; k0 < n; k0 += kThreads) {
             __syncthreads();
-            s_list[tid] = k0 + tid < n ? __ldg(row_list + k0 + tid) : -1;
+            s_list[tid] = k0 == i0 ? r : (k0 + tid < n ? __ldg(row_list + k0 + tid) : -1);
             __syncthreads();
-            const int most = min(kThreads, n - k0);
-            for (int k = 0; k < most; ++k) twice += s_list[k] == r;
+            if (i < n) {
+                const int most = (min(kThreads, n - k0) + 3) / 4;
+                for (int k = 0; k < most; ++k) {
+                    const int4 q = reinterpret_cast<const int4 *>(s_list)[k];
+                    twice += (q.x == r) + (q.y == r) + (q.z == r) + (q.w == r);
+                }
+            }
         }
         if (i >= n) continue;
         Row x = {-1, 0, 0, 0, 0, 0, 0, 0};
@@ -192,7 +235,6 @@ resize_kernel(const gdn_page_table t, const int32_t *row_list, const int32_t *ne
         if (r >= t.rows) {
             bad = GDN_DEV_BAD_SLOT;
         } else if (r >= 0) {
-            const int old = __ldcg(t.seq_lens + r), len = __ldg(new_lens + i);
             if (twice > 1) {
                 bad = GDN_DEV_CONFLICT;
             } else if (!length_ok(t, old) || !length_ok(t, len)) {
@@ -214,29 +256,30 @@ resize_kernel(const gdn_page_table t, const int32_t *row_list, const int32_t *ne
     const int most_gone = s_most[0], most_new = s_most[1];
 
     // 2. pages past the new lengths go back; a warp takes kChunk entries of a row at a time
-    const int64_t gone_units = (int64_t)((most_gone + kChunk - 1) / kChunk) * n;
-    for (int64_t u = gw; u < gone_units; u += kWarps) {
-        const Row x = rows[u % n];
-        const int j0 = x.want + (int)(u / n) * kChunk;
-        if (x.row < 0 || j0 >= x.had) continue;
-        int32_t *const e = t.block_table + x.row * t.table_stride;
-        int id[kChunk / 32];
+    for (int j00 = 0; j00 < most_gone; j00 += kChunk)
+        for (int i = gw; i < n; i += warps) {
+            const Row x = rows[i];
+            const int j0 = x.want + j00;
+            if (x.row < 0 || j0 >= x.had) continue;
+            int32_t *const e = t.block_table + x.row * t.table_stride;
+            int id[kChunk / 32];
 #pragma unroll
-        for (int k = 0; k < kChunk / 32; ++k) {
-            const int j = j0 + k * 32 + lane;
-            id[k] = j < x.had && in_range(j, 1, t.width, status) ? e[j] : -2;
-        }
+            for (int k = 0; k < kChunk / 32; ++k) {
+                const int j = j0 + k * 32 + lane;
+                id[k] = j < x.had && in_range(j, 1, t.width, status) ? e[j] : 0;
+            }
 #pragma unroll
-        for (int k = 0; k < kChunk / 32; ++k) {
-            if (id[k] == -2 && j0 + k * 32 + lane >= x.had) continue;
-            if ((uint32_t)id[k] < (uint32_t)t.num_pages)
-                atomicSub(t.ref_count + id[k], 1);
-            else
-                tell(status, GDN_DEV_BAD_PAGE);
-            e[j0 + k * 32 + lane] = -1;
+            for (int k = 0; k < kChunk / 32; ++k) {
+                const int j = j0 + k * 32 + lane;
+                if (j >= x.had) continue;
+                if ((uint32_t)id[k] < (uint32_t)t.num_pages)
+                    atomicSub(t.ref_count + id[k], 1);
+                else
+                    tell(status, GDN_DEV_BAD_PAGE);
+                if (in_range(j, 1, t.width, status)) e[j] = -1;
+            }
         }
-    }
-    cluster.sync();
+    meet();
 
     // 3. how many pages each row takes, and where its share begins (every block for itself)
     int total = 0, copies = 0;
@@ -262,7 +305,7 @@ resize_kernel(const gdn_page_table t, const int32_t *row_list, const int32_t *ne
             const int before = block_scan(need, s_warp, &sum);
             if (i < n) {
                 x.first = total + before;
-                x.pad = need;
+                x.need = need;
                 rows[i] = x;
             }
             total += sum;
@@ -273,29 +316,42 @@ resize_kernel(const gdn_page_table t, const int32_t *row_list, const int32_t *ne
     //    are exchanged, then it writes its part of the list
     int free_all = 0;
     if (total > 0) {
-        const int share = ((t.num_pages + kCluster - 1) / kCluster + 3) / 4 * 4;
+        const bool vec = ((uintptr_t)t.ref_count & 15) == 0;
+        const int share = ((t.num_pages + blocks - 1) / blocks + kPer - 1) / kPer * kPer;
         const int p0 = min(rank * share, t.num_pages), p1 = min(p0 + share, t.num_pages);
-        int mine = 0;
-#pragma unroll 4
-        for (int p = p0 + tid; p < p1; p += kThreads) mine += __ldcg(t.ref_count + p) <= 0;
-        int sum;
-        block_scan(mine, s_warp, &sum);
-        if (tid == 0) s_free = sum;
-        cluster.sync();
-        int at = 0;
-        for (int k = 0; k < kCluster; ++k) {
-            const int f = *cluster.map_shared_rank(&s_free, k);
-            if (k < rank) at += f;
-            free_all += f;
+        const bool once = blocks > 1 && share <= kThreads * kPer;   // what is counted need not be read again
+        uint32_t in, open = 0;
+        int at = 0, sum;
+        if (blocks > 1) {
+            int mine = 0;
+            for (int p = p0 + tid * kPer; p < p1; p += kThreads * kPer) {
+                const uint32_t used = used_pages(t.ref_count, p, p1, vec, &in);
+                open = in & ~used;
+                mine += __popc(open);
+            }
+            block_scan(mine, s_warp, &sum);
+            if (tid == 0) s_free = sum;
+            cluster.sync();
+            for (int k = 0; k < blocks; ++k) {
+                const int f = *cluster.map_shared_rank(&s_free, k);
+                if (k < rank) at += f;
+                free_all += f;
+            }
         }
-        for (int p = p0; p < p1 && at < total; p += kThreads) {
-            const bool is = p + tid < p1 && __ldcg(t.ref_count + p + tid) <= 0;
-            const int k = at + block_scan(is, s_warp, &sum);
-            if (is && k < total && in_range(k, 1, t.num_pages, status)) ws.free_list[k] = p + tid;
+        for (int q = p0; q < p1 && at < total; q += kThreads * kPer) {
+            const int p = q + tid * kPer;
+            if (!once) {
+                open = ~used_pages(t.ref_count, p, p1, vec, &in);
+                open &= in;
+            }
+            int k = at + block_scan(__popc(open), s_warp, &sum);
+            for (; open && k < total; open &= open - 1, ++k)
+                if (in_range(k, 1, t.num_pages, status)) ws.free_list[k] = p + __ffs(open) - 1;
             at += sum;
         }
+        if (blocks == 1) free_all = at;     // as many as are needed, or all there are
     }
-    cluster.sync();
+    meet();
 
     // 5. rows that fit take their pages
     for (int i0 = 0; i0 < n; i0 += kThreads) {
@@ -304,11 +360,11 @@ resize_kernel(const gdn_page_table t, const int32_t *row_list, const int32_t *ne
         Row x;
         if (i < n) {
             x = rows[i];
-            if (x.row >= 0 && x.pad > 0 && x.first + x.pad > free_all) {
+            if (x.row >= 0 && x.need > 0 && x.first + x.need > free_all) {
                 if (rank == 0) tell(status, GDN_DEV_NO_PAGES);
                 rows[i].row = x.row = -1;
             }
-            copy = x.row >= 0 && x.pad > 0 && x.copied;
+            copy = x.row >= 0 && x.need > 0 && x.copied;
         }
         int sum;
         const int k = copies + block_scan(copy, s_warp, &sum);
@@ -317,28 +373,32 @@ resize_kernel(const gdn_page_table t, const int32_t *row_list, const int32_t *ne
             t.seq_lens[x.row] = x.len;
             if (copy) {
                 atomicSub(t.ref_count + x.last, 1);
-                ws.pairs[k] = make_int2(x.last, ws.free_list[x.first]);
+                ws.pairs[k] = make_int2(x.last, __ldcg(ws.free_list + x.first));
             }
         }
     }
     if (rank == 0 && tid == 0) *ws.count = copies;
     __syncthreads();
-    const int64_t new_units = total > 0 ? (int64_t)((most_new + kChunk - 1) / kChunk) * n : 0;
-    for (int64_t u = gw; u < new_units; u += kWarps) {
-        const Row x = rows[u % n];
-        if (x.row < 0 || x.pad == 0) continue;
-        const int from = x.had - x.copied;        // the entry that gets the row's first page
-        const int j0 = (int)(u / n) * kChunk;
+    for (int j00 = 0; total > 0 && j00 < most_new; j00 += kChunk)
+        for (int i = gw; i < n; i += warps) {
+            const Row x = rows[i];
+            if (x.row < 0 || j00 >= x.need) continue;
+            int32_t *const e = t.block_table + x.row * t.table_stride + x.had - x.copied;
+            int id[kChunk / 32];
 #pragma unroll
-        for (int k = 0; k < kChunk / 32; ++k) {
-            const int j = j0 + k * 32 + lane;
-            if (j >= x.pad || !in_range(from + j, 1, t.width, status)) continue;
-            const int id = ws.free_list[x.first + j];
-            t.block_table[x.row * t.table_stride + from + j] = id;
-            t.ref_count[id] = 1;
+            for (int k = 0; k < kChunk / 32; ++k) {
+                const int j = j00 + k * 32 + lane;
+                id[k] = j < x.need && in_range(x.had - x.copied + j, 1, t.width, status)
+                            ? __ldcg(ws.free_list + x.first + j) : -1;
+            }
+#pragma unroll
+            for (int k = 0; k < kChunk / 32; ++k)
+                if (id[k] >= 0) {
+                    e[j00 + k * 32 + lane] = id[k];
+                    t.ref_count[id[k]] = 1;
+                }
         }
-    }
-    cluster.sync();      // no block leaves while another may read its shared memory
+    if (blocks > 1) cluster.sync();     // no block leaves while another may read its shared memory
 }
 
 // ------------------------------------------------------------------ compact
@@ -349,46 +409,67 @@ struct CompactWork {
     int *used, *open;
 };
 
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
-compact_kernel(const gdn_page_table t, int32_t *const map, const CompactWork ws, int32_t *status)
+__global__ void __launch_bounds__(kThreads, 1)
+compact_kernel(const __grid_constant__ gdn_page_table t, int32_t *const map, const CompactWork ws, int32_t *status)
 {
     cg::cluster_group cluster = cg::this_cluster();
-    const int rank = (int)cluster.block_rank(), tid = threadIdx.x;
+    const int blocks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank(), tid = threadIdx.x;
     __shared__ int s_warp[32];
     __shared__ int s_used;
     launch_dependents();
     const int P = t.num_pages;
-    const int share = ((P + kCluster - 1) / kCluster + 3) / 4 * 4;
+    const bool vec = ((uintptr_t)t.ref_count & 15) == 0;
+    const int share = ((P + blocks - 1) / blocks + kPer - 1) / kPer * kPer;
     const int p0 = min(rank * share, P), p1 = min(p0 + share, P);
+    const bool once = share <= kThreads * kPer;     // what is counted need not be read again
+    // the steps' order: among the blocks, or the threads of the only one
+    auto meet = [&]() {
+        if (blocks > 1) cluster.sync(); else __syncthreads();
+    };
+    uint32_t in = 0, used = 0;
     int mine = 0, sum;
-#pragma unroll 4
-    for (int p = p0 + tid; p < p1; p += kThreads) mine += __ldcg(t.ref_count + p) > 0;
-    block_scan(mine, s_warp, &sum);
-    if (tid == 0) s_used = sum;
-    cluster.sync();
-    int at = 0, U = 0;
-    for (int k = 0; k < kCluster; ++k) {
-        const int f = *cluster.map_shared_rank(&s_used, k);
-        if (k < rank) at += f;
-        U += f;
+    for (int p = p0 + tid * kPer; p < p1; p += kThreads * kPer) {
+        used = used_pages(t.ref_count, p, p1, vec, &in);
+        mine += __popc(used);
+    }
+    const int mine_at = block_scan(mine, s_warp, &sum);
+    int at = 0, U = sum;
+    if (blocks > 1) {
+        if (tid == 0) s_used = sum;
+        cluster.sync();
+        U = 0;
+        for (int k = 0; k < blocks; ++k) {
+            const int f = *cluster.map_shared_rank(&s_used, k);
+            if (k < rank) at += f;
+            U += f;
+        }
     }
     // Of the pages in order, `at` are used before p.  A used page of number >= U is the
     // (at - used before U)-th to move, a free one below U the (p - at)-th place.
-    for (int p = p0; p < p1; p += kThreads) {
-        const int q = p + tid;
-        const bool in = q < p1, is = in && __ldcg(t.ref_count + q) > 0;
-        const int k = at + block_scan(is, s_warp, &sum);
-        at += sum;
-        if (!in) continue;
-        if (q == U) ws.count[1] = k;
-        map[q] = is ? q : -1;
-        if (is && q >= U && in_range(k, 1, P, status)) ws.used[k] = q;
-        if (!is && q < U && in_range(q - k, 1, P, status)) ws.open[q - k] = q;
+    for (int q0 = p0; q0 < p1; q0 += kThreads * kPer) {
+        const int p = q0 + tid * kPer;
+        int k = at + mine_at;
+        if (!once) {
+            used = used_pages(t.ref_count, p, p1, vec, &in);
+            k = at + block_scan(__popc(used), s_warp, &sum);
+            at += sum;
+        }
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+            if (!((in >> e) & 1)) continue;
+            const int q = p + e;
+            const bool is = (used >> e) & 1;
+            if (q == U) ws.count[1] = k;
+            map[q] = is ? q : -1;
+            if (is && q >= U && in_range(k, 1, P, status)) ws.used[k] = q;
+            if (!is && q < U && in_range(q - k, 1, P, status)) ws.open[q - k] = q;
+            k += is;
+        }
     }
-    cluster.sync();
+    meet();
     const int below = U < P ? __ldcg(ws.count + 1) : U;     // used pages of number < U
     const int moves = U - below;
-    for (int k = rank * kThreads + tid; k < moves; k += kCluster * kThreads) {
+    for (int k = rank * kThreads + tid; k < moves; k += blocks * kThreads) {
         const int src = __ldcg(ws.used + below + k), dst = __ldcg(ws.open + k);
         t.ref_count[dst] = __ldcg(t.ref_count + src);
         t.ref_count[src] = 0;
@@ -396,7 +477,7 @@ compact_kernel(const gdn_page_table t, int32_t *const map, const CompactWork ws,
         ws.pairs[k] = make_int2(src, dst);
     }
     if (rank == 0 && tid == 0) ws.count[0] = moves;
-    cluster.sync();      // no block leaves while another may read its shared memory
+    if (blocks > 1) cluster.sync();     // no block leaves while another may read its shared memory
 }
 
 // ------------------------------------------------------------------ fork
@@ -501,7 +582,7 @@ cudaError_t launch_copies(const gdn_page_table &t, const gdn_pool *pools, int n_
         int64_t items = most_pairs * ps.pieces;
         const int32_t *const m = first == 0 ? map : nullptr;
         if (m) {
-            const int64_t renames = (int64_t)t.rows * t.width / kCopyThreads + 1;
+            const int64_t renames = t.rows / (kCopyThreads / 32) + 1;
             items = items > renames ? items : renames;
         }
         const cudaError_t e = launch_dependent(copy_pairs_kernel, dim3(copy_blocks(items)),
@@ -510,6 +591,62 @@ cudaError_t launch_copies(const gdn_page_table &t, const gdn_pool *pools, int n_
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
+}
+
+// Blocks of a large plan: sixteen where the device can place such a cluster (more than the eight
+// that every one can), asked once per device.
+template <typename K>
+cudaError_t largest_cluster(K kernel, std::atomic<int> (&known)[32], int *blocks)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    *blocks = dev < 32 ? known[dev].load(std::memory_order_acquire) : 0;
+    if (*blocks > 0) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kCluster);
+    cfg.blockDim = dim3(kThreads);
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = kCluster;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
+        cudaGetLastError();
+        *blocks = 8;
+    } else {
+        *blocks = kCluster;
+    }
+    if (dev < 32) known[dev].store(*blocks, std::memory_order_release);
+    return cudaSuccess;
+}
+
+template <typename... KA, typename... A>
+cudaError_t launch_cluster(void (*kernel)(KA...), int blocks, cudaStream_t stream, A &&...args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = blocks;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, KA(args)...);
+}
+
+// One block for tables that it passes over at once and lists that may change some ten thousand
+// entries; else a cluster.  Two calls of 16 to 200 rows on rows of 129 entries: 16, 25 (128 rows:
+// 16512 entries), 55 us on one block, 21, 27, 36 us on a cluster.
+bool small_plan(const gdn_page_table &t, int n)
+{
+    return t.num_pages <= kThreads * kPer && (int64_t)n * t.width <= kThreads * 24;
 }
 
 uint64_t up16(uint64_t x) { return (x + 15) / 16 * 16; }
@@ -538,8 +675,11 @@ cudaError_t launch_page_resize(const gdn_page_table &t, const int32_t *row_list,
     unsigned char *const r = w + 16 + up16((uint64_t)n * sizeof(int2));
     ws.rows = reinterpret_cast<Row *>(r);
     ws.free_list = reinterpret_cast<int *>(r + (uint64_t)kCluster * n * sizeof(Row));
-    resize_kernel<<<kCluster, kThreads, 0, stream>>>(t, row_list, new_lens, n, ws, dev_status);
-    const cudaError_t e = cudaGetLastError();
+    static std::atomic<int> known[32];
+    int blocks = 1;
+    cudaError_t e = small_plan(t, n) ? cudaSuccess : largest_cluster(resize_kernel, known, &blocks);
+    if (e == cudaSuccess)
+        e = launch_cluster(resize_kernel, blocks, stream, t, row_list, new_lens, n, ws, dev_status);
     if (e != cudaSuccess) return e;
     return launch_copies(t, pools, n_pools, ws.pairs, ws.count, n, nullptr, dev_status, stream);
 }
@@ -556,8 +696,10 @@ cudaError_t launch_page_compact(const gdn_page_table &t, int32_t *page_map, cons
     unsigned char *const u = w + 16 + up16((uint64_t)t.num_pages * sizeof(int2));
     ws.used = reinterpret_cast<int *>(u);
     ws.open = reinterpret_cast<int *>(u + up16((uint64_t)t.num_pages * 4));
-    compact_kernel<<<kCluster, kThreads, 0, stream>>>(t, page_map, ws, dev_status);
-    const cudaError_t e = cudaGetLastError();
+    static std::atomic<int> known[32];
+    int blocks = 1;
+    cudaError_t e = small_plan(t, 0) ? cudaSuccess : largest_cluster(compact_kernel, known, &blocks);
+    if (e == cudaSuccess) e = launch_cluster(compact_kernel, blocks, stream, t, page_map, ws, dev_status);
     if (e != cudaSuccess) return e;
     return launch_copies(t, pools, n_pools, ws.pairs, ws.count, t.num_pages / 2, page_map,
                          dev_status, stream);
