@@ -56,12 +56,28 @@ def _on_stream(first):
                     raise ValueError(f"stream is on {stream.device}, {first} on {t.device}")
                 with torch.cuda.stream(stream):
                     return f(*args, **kw)
-            if t.device.index != torch.cuda.current_device():
+            if t.get_device() != torch._C._cuda_getDevice():
                 with torch.cuda.device(t.device):
                     return f(*args, **kw)
             return f(*args, **kw)
         return call
     return wrap
+
+
+def _stream(device):
+    """The current stream of `device`, as an address (torch.cuda.current_stream would make an
+    object of it first, at a third of a small call's host time)."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+@functools.lru_cache(maxsize=256)
+def _attn_workspace(lib, device, *sizes):
+    """gdn_paged_attn_workspace_size: it depends on the device and these sizes alone."""
+    return lib.gdn_paged_attn_workspace_size(*sizes)
 
 
 def _tensor(name, t, dtype, shape, device, dense=True):
@@ -81,7 +97,8 @@ def _ints(name, t, n, device):
     """An int32 list that the call only reads."""
     if t is None:
         return None
-    return _tensor(name, t, _I32, (n,), device, dense=False).contiguous()
+    t = _tensor(name, t, _I32, (n,), device, dense=False)
+    return t if t.is_contiguous() else t.contiguous()
 
 
 def _rows_of(block_table, device):
@@ -115,8 +132,7 @@ def _cache(k_cache, v_cache, block_table, seq_lens, k_scale, v_scale):
     if v_scale is not None:
         _tensor("v_scale", v_scale, torch.float32, (H,), device)
     return _Cache(k_cache.data_ptr(), v_cache.data_ptr(), st[0], st[1], st[2],
-                  None if k_scale is None else k_scale.data_ptr(),
-                  None if v_scale is None else v_scale.data_ptr(), block_table.data_ptr(),
+                  _at(k_scale), _at(v_scale), block_table.data_ptr(),
                   seq_lens.data_ptr(), stride, rows, width, P, S, H, D, code)
 
 
@@ -180,9 +196,9 @@ def gdn_kv_append(k, v, k_cache, v_cache, block_table, seq_lens, slots=None, row
         B = k.shape[0] if k.dim() == 4 else cache.rows
     slots = _ints("slots", slots, B, device)
     row_offsets = _ints("row_offsets", row_offsets, B + 1, device)
-    _raise(b.lib().gdn_kv_append(b._ptr(k), b._ptr(v), kt, kh, vt, vh, ctypes.byref(cache),
-                                 b._ptr(slots), b._ptr(row_offsets), B, N, dt,
-                                 b._ptr(dev_status), b._stream(None)), "gdn_kv_append")
+    _raise(b.lib().gdn_kv_append(_at(k), _at(v), kt, kh, vt, vh, ctypes.byref(cache),
+                                 _at(slots), _at(row_offsets), B, N, dt,
+                                 _at(dev_status), _stream(device)), "gdn_kv_append")
     return k_cache, v_cache
 
 
@@ -219,21 +235,21 @@ def gdn_paged_attn(q, k_cache, v_cache, block_table, seq_lens, slots=None, *, sc
         else:
             lse = torch.full((B, T, Hq), -math.inf, device=device) if return_lse else None
     if out is None:
-        out = torch.empty((B, T, Hq, D), dtype=q.dtype, device=device)
+        out = q.new_empty((B, T, Hq, D))
         flags = b.GDN_ZERO_PADDING
     else:
         _tensor("out", out, q.dtype, (B, T, Hq, D), device)
     if lse is not None:
         _tensor("lse", lse, torch.float32, (B, T, Hq), device)
     elif return_lse:
-        lse = torch.empty((B, T, Hq), dtype=torch.float32, device=device)
+        lse = q.new_empty((B, T, Hq), dtype=torch.float32)
     L = b.lib()
-    nbytes = L.gdn_paged_attn_workspace_size(B, T, Hq, cache.heads, cache.head_dim, cache.dtype)
-    ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
-    _raise(L.gdn_paged_attn(b._ptr(q), qt, qh, ctypes.byref(cache), b._ptr(slots), B, T, Hq, dt,
+    nbytes = _attn_workspace(L, device, B, T, Hq, cache.heads, cache.head_dim, cache.dtype)
+    ws = q.new_empty((max(nbytes, 16),), dtype=torch.uint8)
+    _raise(L.gdn_paged_attn(_at(q), qt, qh, ctypes.byref(cache), _at(slots), B, T, Hq, dt,
                             1.0 / math.sqrt(D) if scale is None else float(scale), int(window),
-                            b._ptr(out), b._ptr(lse), flags, b._ptr(ws), nbytes,
-                            b._ptr(dev_status), b._stream(None)), "gdn_paged_attn")
+                            _at(out), _at(lse), flags, _at(ws), nbytes,
+                            _at(dev_status), _stream(device)), "gdn_paged_attn")
     return out if lse is None else (out, lse)
 
 
@@ -288,9 +304,9 @@ def gdn_page_resize(block_table, ref_count, seq_lens, row_list, new_lens, page_s
     arr, count = _pools(pools, t.num_pages, device)
     L = b.lib()
     nbytes = L.gdn_page_workspace_size(t.num_pages, max(n, 1))
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    _raise(L.gdn_page_resize(ctypes.byref(t), b._ptr(row_list), b._ptr(new_lens), n, arr, count,
-                             b._ptr(ws), nbytes, b._ptr(dev_status), b._stream(None)),
+    ws = block_table.new_empty((nbytes,), dtype=torch.uint8)
+    _raise(L.gdn_page_resize(ctypes.byref(t), _at(row_list), _at(new_lens), n, arr, count,
+                             _at(ws), nbytes, _at(dev_status), _stream(device)),
            "gdn_page_resize")
     return block_table, ref_count, seq_lens
 
@@ -311,8 +327,8 @@ def gdn_page_fork(block_table, ref_count, seq_lens, parents, children, page_size
     parents = _ints("parents", parents, n, device)
     children = _ints("children", children, n, device)
     arr, count = _pools(pools, t.rows, device)
-    _raise(b.lib().gdn_page_fork(ctypes.byref(t), b._ptr(parents), b._ptr(children), n, arr,
-                                 count, b._ptr(dev_status), b._stream(None)), "gdn_page_fork")
+    _raise(b.lib().gdn_page_fork(ctypes.byref(t), _at(parents), _at(children), n, arr,
+                                 count, _at(dev_status), _stream(device)), "gdn_page_fork")
     return block_table, ref_count, seq_lens
 
 
@@ -328,12 +344,12 @@ def gdn_page_compact(block_table, ref_count, seq_lens, page_size: int, pools=(),
     t = _table(block_table, ref_count, seq_lens, page_size)
     arr, count = _pools(pools, t.num_pages, device)
     if page_map is None:
-        page_map = torch.empty(t.num_pages, dtype=_I32, device=device)
+        page_map = block_table.new_empty((t.num_pages,))
     else:
         _tensor("page_map", page_map, _I32, (t.num_pages,), device)
     L = b.lib()
     nbytes = L.gdn_page_workspace_size(t.num_pages, 0)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    _raise(L.gdn_page_compact(ctypes.byref(t), b._ptr(page_map), arr, count, b._ptr(ws), nbytes,
-                              b._ptr(dev_status), b._stream(None)), "gdn_page_compact")
+    ws = block_table.new_empty((nbytes,), dtype=torch.uint8)
+    _raise(L.gdn_page_compact(ctypes.byref(t), _at(page_map), arr, count, _at(ws), nbytes,
+                              _at(dev_status), _stream(device)), "gdn_page_compact")
     return page_map
