@@ -378,7 +378,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                     d.last = !more; d.place = place;
                     s_desc[st] = d;
                 }
-                const uint32_t extra = i == 0 && c == 0 && fw == 0 && gdn::test_stall_requested(a.dev_status) ? 16 : 0;
+                const uint32_t extra = place == kUnitCost && fw == 0 && gdn::test_stall_requested(a.dev_status) ? 16 : 0;
                 sm100::mbar_arrive_expect_tx(full0 + 8 * st, (uint32_t)(boxes * box * C::RB * 2) + extra);
             }
             __syncwarp();

@@ -100,9 +100,10 @@ enum {
     GDN_DEV_BAD_LENGTH = 32,  /* a length outside what a row of the page table holds */
     GDN_DEV_CONFLICT = 64,    /* a row listed twice, or as a child and as a parent: left undone */
     GDN_DEV_NO_PAGES = 128,   /* too few free pages: the rows that did not fit are left undone */
-    /* Checked builds only, set by the CALLER in *dev_status before a gdn_decode or a
-     * chunked gdn_prefill call: the persistent decode kernel, or the chunked prefill
-     * kernel's first q/k stage, posts 16 bytes more than its copies deliver (the per-key
+    /* Checked builds only, set by the CALLER in *dev_status before a gdn_decode, a
+     * gdn_paged_attn or a chunked gdn_prefill call: the persistent decode kernel, the call's
+     * first tile of pages, or the chunked prefill kernel's first q/k stage, posts 16 bytes
+     * more than its copies deliver (the per-key
      * decay kernel's first CTA waits for its first W/U~ MMA group on a barrier that nothing
      * arrives on), so the waits run out after their bound (about a second), GDN_DEV_TIMEOUT
      * is set and the kernel returns.  Exercises the timeout path without a fault; ignored by

@@ -1,0 +1,244 @@
+"""The paged cache's calls as programs use them: captured graphs, several streams, the checked
+build, a wait that runs out."""
+import time
+
+import pytest
+import torch
+
+from _paged import Case, attend, check_attend
+
+pytestmark = pytest.mark.gpu
+
+E4M3 = torch.float8_e4m3fn
+
+
+@pytest.fixture(scope="module")
+def gdn():
+    import gated_deltanet_state_gdn_b200 as g
+    from gated_deltanet_state_gdn_b200 import build
+    build.build(checked=True)   # rebuilds only when missing or older than the sources
+    product = g._binding.LIB_PATH
+    yield g
+    g.use_library(product)
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+class Server:
+    """A cache and the tensors of one decoding step over it."""
+
+    def __init__(self, seed, rows=6, T=2, H=2, Hq=8, D=128, page=16, cache=torch.bfloat16):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        self.T, self.page, self.H, self.D = T, page, H, D
+        self.P = 80
+        self.k, self.v = (torch.randn(self.P, page, H, D, device="cuda", generator=g).to(torch.bfloat16).to(cache)
+                          for _ in range(2))
+        self.table = torch.full((rows, 20), -1, dtype=torch.int32, device="cuda")
+        self.ref, self.seq = ints([0] * self.P), ints([0] * rows)
+        self.slots = ints(list(range(rows))[::-1])
+        self.lens = ints([5, 17, 40, 3, 64, 90])
+        self.rows = ints(list(range(rows)))
+        new = lambda *s: torch.randn(*s, device="cuda", generator=g).to(torch.bfloat16)  # noqa: E731
+        self.q, self.kn, self.vn = new(rows, T, Hq, D), new(rows, T, H, D), new(rows, T, H, D)
+        self.out = torch.zeros_like(self.q)
+        self.status = ints([0])
+
+    def start(self, gdn):
+        gdn.gdn_page_resize(self.table, self.ref, self.seq, self.rows, self.lens, self.page, [self.k, self.v])
+
+    def step(self, gdn, **kw):
+        gdn.gdn_page_resize(self.table, self.ref, self.seq, self.rows, self.lens, self.page, [self.k, self.v],
+                            dev_status=self.status, **kw)
+        gdn.gdn_kv_append(self.kn, self.vn, self.k, self.v, self.table, self.seq, self.slots, dev_status=self.status,
+                          **kw)
+        return gdn.gdn_paged_attn(self.q, self.k, self.v, self.table, self.seq, self.slots, out=self.out,
+                                  dev_status=self.status, **kw)
+
+    def everything(self):
+        return [x.clone() for x in (self.table, self.ref, self.seq, self.k, self.v, self.out)]
+
+
+def same(a, b):
+    return all(torch.equal(x.view(torch.uint8) if x.dtype == E4M3 else x,
+                           y.view(torch.uint8) if y.dtype == E4M3 else y) for x, y in zip(a, b))
+
+
+def advance(s, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    s.lens += s.T
+    for x in (s.q, s.kn, s.vn):
+        x.copy_(torch.randn(x.shape, device="cuda", generator=g))
+
+
+@pytest.mark.parametrize("cache", [torch.bfloat16, E4M3])
+def test_captured_step_replays(gdn, cache):
+    """A whole step captured once and replayed on new inputs does what the calls do one by one."""
+    a, b = Server(1, cache=cache), Server(1, cache=cache)
+    a.start(gdn)
+    b.start(gdn)
+    for s in (a, b):
+        advance(s, 7)
+    a.step(gdn)                         # warm-up outside the capture
+    b.step(gdn)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    advance(a, 8)
+    advance(b, 8)
+    keep = a.everything()
+    with torch.cuda.graph(graph):
+        a.step(gdn)
+    assert same(keep, a.everything())   # a capture runs nothing
+    for n in range(5):
+        graph.replay()
+        b.step(gdn)
+        torch.cuda.synchronize()
+        assert same(a.everything(), b.everything()), n
+        for s in (a, b):
+            advance(s, 20 + n)
+    assert int(a.status.item()) == 0
+
+
+def test_two_graphs_and_two_streams_at_once(gdn):
+    """Two captured steps replayed at the same time, and two eager ones on streams of their own,
+    do not meet."""
+    servers = [Server(s) for s in range(4)]
+    alone = [Server(s) for s in range(4)]
+    for s in servers + alone:
+        s.start(gdn)
+        advance(s, 3)
+        s.step(gdn)
+        advance(s, 4)
+    for s in alone:
+        s.step(gdn)
+    torch.cuda.synchronize()
+    graphs = []
+    for s in servers[:2]:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            s.step(gdn)
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    torch.cuda.synchronize()
+    for g, st in zip(graphs, streams):
+        with torch.cuda.stream(st):
+            g.replay()
+    for s, st in zip(servers[2:], streams[2:]):
+        s.step(gdn, stream=st)
+    torch.cuda.synchronize()
+    for s, x in zip(servers, alone):
+        assert same(s.everything(), x.everything())
+
+
+def test_given_stream_orders_the_call(gdn):
+    """`stream` runs the whole call there, copies of its arguments included: inputs that the stream
+    itself makes late are seen, on a stream that is not the current one."""
+    c = Case(3, [500, 20, 90], T=1, D=128)
+    want = c.attend(gdn)
+    args = [c.to(x) for x in (c.q, c.k, c.v, c.table, c.seq, c.slots)]
+    q = torch.zeros(3, 4, 1, 128, dtype=torch.bfloat16, device="cuda").transpose(1, 2)[:, :, ::1]
+    late = torch.zeros(3, 1, 4, 132, dtype=torch.bfloat16, device="cuda")[..., 1:129]   # off its alignment
+    st = torch.cuda.Stream()
+    big = torch.zeros(1 << 28, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.stream(st):
+        for _ in range(20):
+            big.add_(1.0)               # keeps the stream busy for a while
+        late.copy_(args[0])
+        q.copy_(args[0])
+    got = gdn.gdn_paged_attn(late, *args[1:], return_lse=True, stream=st)
+    got2 = gdn.gdn_paged_attn(q, *args[1:], return_lse=True, stream=st)
+    st.synchronize()
+    assert same(got, want) and same(got2, want)
+
+
+def test_wrong_devices_are_refused(gdn):
+    c = Case(4, [5])
+    args = [c.to(x) for x in (c.q, c.k, c.v, c.table, c.seq, c.slots)]
+    for i in range(6):
+        bad = list(args)
+        bad[i] = args[i].cpu()
+        with pytest.raises(TypeError):
+            gdn.gdn_paged_attn(*bad)
+    with pytest.raises(ValueError):
+        gdn.gdn_paged_attn(args[0], args[1], args[2].transpose(1, 2).contiguous().transpose(1, 2), *args[3:])
+    with pytest.raises(ValueError):
+        gdn.gdn_paged_attn(args[0][..., ::2], *args[1:])
+    with pytest.raises(TypeError):
+        gdn.gdn_paged_attn(args[0].float(), *args[1:])
+    with pytest.raises(TypeError):
+        gdn.gdn_paged_attn(*args[:5], args[5].long())
+    with pytest.raises(gdn.GdnError):
+        gdn.gdn_paged_attn(args[0].half(), *args[1:])
+    with pytest.raises(gdn.GdnError):
+        gdn.gdn_paged_attn(args[0].expand(1, 17, 4, 64).contiguous(), *args[1:])
+    with pytest.raises(ValueError):
+        gdn.gdn_paged_attn(*args, lse=torch.zeros(1, 1, 3, device="cuda"))
+
+
+def both(gdn, fn):
+    """fn(status) through the product library, then through the checked build."""
+    product = gdn._binding.LIB_PATH
+    r0 = fn(None)
+    st = ints([0])
+    gdn.use_library(gdn.CHECKED_LIB_PATH)
+    try:
+        r1 = fn(st)
+    finally:
+        gdn.use_library(product)
+    return r0, r1, int(st.item())
+
+
+@pytest.mark.parametrize("cache", [torch.bfloat16, torch.float16, E4M3])
+@pytest.mark.parametrize("D,Hq,T,page", [(64, 4, 1, 16), (128, 4, 5, 24), (48, 32, 2, 1), (256, 16, 4, 272),
+                                         (192, 2, 1, 16)])
+def test_attention_in_bounds(gdn, cache, D, Hq, T, page):
+    dtype = torch.float16 if cache == torch.float16 else torch.bfloat16
+    c = Case(D, [1, 0, 900, 17, 64, 3], D=D, Hq=Hq, T=T, page=page, dtype=dtype, cache=cache, pad=(3,))
+    r0, r1, st = both(gdn, lambda status: c.attend(gdn, window=300, dev_status=status))
+    assert st == 0 and same(r0, r1)
+
+
+@pytest.mark.parametrize("cache", [torch.bfloat16, E4M3])
+def test_append_and_tables_in_bounds(gdn, cache):
+    def run(status):
+        s = Server(5, cache=cache)
+        s.status = status
+        s.start(gdn)
+        advance(s, 1)
+        s.step(gdn)
+        state = torch.arange(6 * 1001, device="cuda", dtype=torch.float32).reshape(6, 1001)
+        gdn.gdn_page_fork(s.table, s.ref, s.seq, ints([1, 2, -1]), ints([5, 0, 3]), s.page, [state], dev_status=status)
+        s.lens += 3
+        gdn.gdn_page_resize(s.table, s.ref, s.seq, s.rows, s.lens, s.page, [s.k, s.v], dev_status=status)
+        gdn.gdn_page_resize(s.table, s.ref, s.seq, ints([3, 0]), ints([0, 7]), s.page, [s.k, s.v], dev_status=status)
+        to = gdn.gdn_page_compact(s.table, s.ref, s.seq, s.page, [s.k, s.v], dev_status=status)
+        return s.everything() + [state, to]
+    r0, r1, st = both(gdn, run)
+    assert st == 0 and same(r0, r1)
+
+
+def test_attention_wait_runs_out_on_request(gdn):
+    """GDN_DEV_TEST_STALL makes the first tile of the call expect 16 bytes more than its copies
+    deliver: its waits run out after about a second, GDN_DEV_TIMEOUT is set, every warp leaves,
+    and a normal call on the same context then matches the product library bit for bit."""
+    c = Case(6, [700, 40], T=2, D=128)
+    want = c.attend(gdn)
+    product = gdn._binding.LIB_PATH
+    gdn.use_library(gdn.CHECKED_LIB_PATH)
+    try:
+        st = ints([gdn.GDN_DEV_TEST_STALL])
+        t0 = time.time()
+        c.attend(gdn, dev_status=st)
+        torch.cuda.synchronize()
+        took = time.time() - t0
+        s = int(st.item())
+        assert s & gdn.GDN_DEV_TIMEOUT and not s & gdn.GDN_DEV_BOUNDS and took < 60
+        st2 = ints([0])
+        got = c.attend(gdn, dev_status=st2)
+        assert int(st2.item()) == 0
+    finally:
+        gdn.use_library(product)
+    assert same(got, want)
+    check_attend(c, got, attend(c))
