@@ -71,7 +71,8 @@ struct Cfg {
     static constexpr int FW = TILE / 32 / FETCH;     // 32 tokens each of a warp's share
     // tokens a warp takes at a time: two blocks of 16, twice the independent products, where it
     // has them and the registers hold them
-    static constexpr int STEP = ESZ == 1 || DP == 64 ? 32 : 16;
+    static constexpr int STEP = ESZ == 1 && DP == 64 && WT == 4 ? 64 : (ESZ == 1 || DP == 64 ? 32 : 16);
+    using Mask = typename std::conditional<STEP == 64, uint64_t, uint32_t>::type;   // a bit a token
     static constexpr int NS = TILE / WT / STEP;      // such steps of a warp in a tile
     static constexpr int NX = STEP / 8;              // blocks of 8 columns of scores
     static constexpr int DW = DP / WD;               // dimensions a warp accumulates
@@ -90,7 +91,9 @@ struct Split {              // a unit whose parts lie in blocks [c0, c1]
 };
 
 // What a unit costs beside its tiles (its queries, its end), in tiles, when work is dealt out.
-constexpr int kUnitCost = 2;
+// 256 rows of 1 to 4096 tokens, four tokens each, with 0, 2, 3, 4: 358, 336, 320, 317 us; one token
+// each over e4m3: 241, 218, 208, 205 us; equal rows do not care, few tiles in all lose with more.
+constexpr int kUnitCost = 3;
 
 // W places in a row dealt to G blocks: the first `more` get one more than the others
 struct Deal {
@@ -550,8 +553,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
 #pragma unroll 1
         for (int s = 0; s < C::NS; ++s) {
             const int tok = (s * C::WT + wt) * C::STEP;
-            constexpr uint32_t kAll = C::STEP == 32 ? 0xffffffffu : 0xffffu;
-            const uint32_t ok = (s_valid[st][tok >> 5] >> (tok & 31)) & kAll;
+            using Mask = typename C::Mask;
+            constexpr Mask kAll = (Mask)~(Mask)0 >> (sizeof(Mask) * 8 - C::STEP);
+            Mask ok = (s_valid[st][tok >> 5] >> (tok & 31)) & kAll;
+            if constexpr (C::STEP == 64) ok |= (Mask)s_valid[st][(tok >> 5) + 1] << 32;
             if (ok == 0) continue;
             const int j0 = d.base + tok;
             const bool ragged = j0 + C::STEP - 1 > see_all || j0 < see_from;    // rows may see different tokens
@@ -692,20 +697,24 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                         }
                     }
                 } else {
-                    const int vr = tok + token_of<C>(2 * (lane >> 4) + ((lane >> 1) & 1),
-                                                     2 * ((lane >> 2) & 3) + (lane & 1));
 #pragma unroll
-                    for (int n = 0; n < C::DW / 8; n += 2) {
-                        uint32_t b[4];
-                        ldmatrix_b8_x2_trans(b, vs + piece<C>(vr, wd * (C::DW / 16) + n / 2));
+                    for (int v = 0; v < NX / 4; ++v) {      // 32 tokens
+                        const int vr = tok + 32 * v + token_of<C>(2 * (lane >> 4) + ((lane >> 1) & 1),
+                                                                  2 * ((lane >> 2) & 3) + (lane & 1));
 #pragma unroll
-                        for (int u = 0; u < 2; ++u)
+                        for (int n = 0; n < C::DW / 8; n += 2) {
+                            uint32_t b[4];
+                            ldmatrix_b8_x2_trans(b, vs + piece<C>(vr, wd * (C::DW / 16) + n / 2));
 #pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                uint32_t b0, b1;
-                                e4m3x4_to_f16x2(scrub(b[2 * u + k]), b0, b1);
-                                mma_16816<false>(o[n + k], p[u][0], p[u][1], p[u][2], p[u][3], b0, b1);
-                            }
+                            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                                for (int k = 0; k < 2; ++k) {
+                                    const uint32_t(&q)[4] = p[2 * v + u];
+                                    uint32_t b0, b1;
+                                    e4m3x4_to_f16x2(scrub(b[2 * u + k]), b0, b1);
+                                    mma_16816<false>(o[n + k], q[0], q[1], q[2], q[3], b0, b1);
+                                }
+                        }
                     }
                 }
                 return bad;
@@ -871,15 +880,18 @@ constexpr int kJoinRows = kJoin / 32;
 template <int DP>
 __global__ void __launch_bounds__(kJoin)
 paged_attn_join_kernel(const GdnAttnArgs a, const int RT, const int RMAX, const int per,
-                       const Split *const splits, const float2 *const part_ml, const float *const part_o)
+                       const int blocks, const Split *const splits, const float2 *const part_ml, const float *const part_o)
 {
     __shared__ float s_w[kMaxBlocks];                   // weights of the parts
     __shared__ float s_red[2][kJoin / 32];
     __shared__ float4 s_o[kJoinGroups][16];
     wait_primary();
     const Split sp = splits[blockIdx.x];
-    if (sp.c1 < 0) return;
     const int H = a.cache.heads, D = a.cache.head_dim, group = a.Hq / H;
+    // (a block that gave up waiting wrote nothing: what is there then need not make sense)
+    if (sp.c1 < 0 || sp.c0 < 0 || sp.c0 > sp.c1 || sp.c1 >= blocks || (uint32_t)sp.b >= (uint32_t)a.B ||
+        (uint32_t)sp.u_lo >= (uint32_t)(H * RT))
+        return;
     const int h = sp.u_lo / RT, rt = sp.u_lo - h * RT;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int np = sp.c1 - sp.c0 + 1;
@@ -1137,7 +1149,7 @@ cudaError_t launch(const GdnAttnArgs &a, cudaStream_t stream)
     const int per = units * kFew >= blocks ? kJoinRows : 1;
     return launch_dependent(paged_attn_join_kernel<DP>,
                             dim3(n_splits, (rows + per - 1) / per, per == 1 ? DP / 64 : 1), dim3(kJoin), 0,
-                            stream, a, y.RT, y.RMAX, per, splits, ml, o);
+                            stream, a, y.RT, y.RMAX, per, blocks, splits, ml, o);
 }
 
 // A box starts on 128 bytes of shared memory: 64-byte rows need an even number of tokens, so
