@@ -55,24 +55,25 @@ __device__ __forceinline__ bool length_ok(const gdn_page_table &t, int len)
 }
 
 // exclusive prefix sum over the block's threads; *total is the same in all
-__device__ __forceinline__ int block_scan(int x, int *s_warp, int *total)
+template <typename T>
+__device__ __forceinline__ T block_scan(T x, T *s_warp, T *total)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-    int incl = x;
+    T incl = x;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, d);
+        const T y = __shfl_up_sync(0xffffffffu, incl, d);
         if (lane >= d) incl += y;
     }
     if (lane == 31) s_warp[warp] = incl;
     __syncthreads();
-    int w = lane < nw ? s_warp[lane] : 0, wi = w;
+    T w = lane < nw ? s_warp[lane] : 0, wi = w;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, wi, d);
+        const T y = __shfl_up_sync(0xffffffffu, wi, d);
         if (lane >= d) wi += y;
     }
-    const int before = __shfl_sync(0xffffffffu, wi - w, warp);
+    const T before = __shfl_sync(0xffffffffu, wi - w, warp);
     *total = __shfl_sync(0xffffffffu, wi, 31);
     __syncthreads();                    // s_warp is used again
     return before + incl - x;
@@ -199,6 +200,7 @@ resize_kernel(const __grid_constant__ gdn_page_table t, const int32_t *row_list,
     const int warps = blocks * (kThreads / 32), gw = (tid >> 5) * blocks + rank;    // of the cluster
     __shared__ __align__(16) int s_list[kThreads];
     __shared__ int s_warp[32];
+    __shared__ long long s_wide[32];
     __shared__ int s_most[2];
     __shared__ int s_free;
     __shared__ Row s_rows[kNear];
@@ -281,8 +283,10 @@ resize_kernel(const __grid_constant__ gdn_page_table t, const int32_t *row_list,
         }
     meet();
 
-    // 3. how many pages each row takes, and where its share begins (every block for itself)
-    int total = 0, copies = 0;
+    // 3. how many pages each row takes, and where its share begins (every block for itself); what is
+    //    asked for may pass 32 bits, what there is does not
+    long long total = 0;
+    int copies = 0;
     if (most_new > 0) {
         for (int i0 = 0; i0 < n; i0 += kThreads) {
             const int i = i0 + tid;
@@ -301,10 +305,10 @@ resize_kernel(const __grid_constant__ gdn_page_table t, const int32_t *row_list,
                 }
                 if (x.row >= 0) need = max(x.want - x.had, 0) + x.copied;
             }
-            int sum;
-            const int before = block_scan(need, s_warp, &sum);
+            long long sum;
+            const long long before = total + block_scan<long long>(need, s_wide, &sum);
             if (i < n) {
-                x.first = total + before;
+                x.first = (int)(before < t.num_pages ? before : t.num_pages);
                 x.need = need;
                 rows[i] = x;
             }
@@ -329,7 +333,7 @@ resize_kernel(const __grid_constant__ gdn_page_table t, const int32_t *row_list,
                 open = in & ~used;
                 mine += __popc(open);
             }
-            block_scan(mine, s_warp, &sum);
+            block_scan<int>(mine, s_warp, &sum);
             if (tid == 0) s_free = sum;
             cluster.sync();
             for (int k = 0; k < blocks; ++k) {
@@ -344,7 +348,7 @@ resize_kernel(const __grid_constant__ gdn_page_table t, const int32_t *row_list,
                 open = ~used_pages(t.ref_count, p, p1, vec, &in);
                 open &= in;
             }
-            int k = at + block_scan(__popc(open), s_warp, &sum);
+            int k = at + block_scan<int>(__popc(open), s_warp, &sum);
             for (; open && k < total; open &= open - 1, ++k)
                 if (in_range(k, 1, t.num_pages, status)) ws.free_list[k] = p + __ffs(open) - 1;
             at += sum;
@@ -360,14 +364,14 @@ resize_kernel(const __grid_constant__ gdn_page_table t, const int32_t *row_list,
         Row x;
         if (i < n) {
             x = rows[i];
-            if (x.row >= 0 && x.need > 0 && x.first + x.need > free_all) {
+            if (x.row >= 0 && x.need > free_all - x.first && x.need > 0) {
                 if (rank == 0) tell(status, GDN_DEV_NO_PAGES);
                 rows[i].row = x.row = -1;
             }
             copy = x.row >= 0 && x.need > 0 && x.copied;
         }
         int sum;
-        const int k = copies + block_scan(copy, s_warp, &sum);
+        const int k = copies + block_scan<int>(copy, s_warp, &sum);
         copies += sum;
         if (rank == 0 && i < n && x.row >= 0) {
             t.seq_lens[x.row] = x.len;
@@ -432,7 +436,7 @@ compact_kernel(const __grid_constant__ gdn_page_table t, int32_t *const map, con
         used = used_pages(t.ref_count, p, p1, vec, &in);
         mine += __popc(used);
     }
-    const int mine_at = block_scan(mine, s_warp, &sum);
+    const int mine_at = block_scan<int>(mine, s_warp, &sum);
     int at = 0, U = sum;
     if (blocks > 1) {
         if (tid == 0) s_used = sum;
@@ -451,7 +455,7 @@ compact_kernel(const __grid_constant__ gdn_page_table t, int32_t *const map, con
         int k = at + mine_at;
         if (!once) {
             used = used_pages(t.ref_count, p, p1, vec, &in);
-            k = at + block_scan(__popc(used), s_warp, &sum);
+            k = at + block_scan<int>(__popc(used), s_warp, &sum);
             at += sum;
         }
 #pragma unroll

@@ -187,6 +187,20 @@ def test_many_rows_and_pages(gdn):
     assert s.model.status == 0
 
 
+def test_more_asked_for_than_32_bits_count(gdn):
+    """2200 rows that ask for a million pages each: more than 2^31 in all, of a hundred there are.
+    The row ahead of them fits; the ones behind the shortage wait, however little they ask for."""
+    rows, width, P = 2203, 1 << 20, 100
+    table = torch.full((rows, width), -1, dtype=torch.int32, device="cuda")
+    ref, seq, st = ints([0] * P), ints([0] * rows), ints([0])
+    lens = [60] + [width] * 2200 + [3, 0]
+    gdn.gdn_page_resize(table, ref, seq, ints(list(range(rows))), ints(lens), 1, dev_status=st)
+    assert int(st.item()) == gdn.GDN_DEV_NO_PAGES
+    assert seq.tolist() == [60] + [0] * 2202
+    assert ref.tolist() == [1] * 60 + [0] * 40 and table[0, :61].tolist() == list(range(60)) + [-1]
+    assert int((table[1:] != -1).sum()) == 0
+
+
 def test_no_rows(gdn):
     s = State(3, 3, 5, 4)
     s.resize(gdn, [], [])
