@@ -81,9 +81,10 @@ struct Cfg {
     static_assert(WT >= 1 && NS >= 1, "four warps");
 };
 
-struct Desc {
-    int b, u, base, len, tile, nt, last;    // last: of the block's run
-    int64_t place;                          // in the deal
+struct alignas(16) Desc {
+    int b, h, rt, base;             // request, head, block of rows, first position
+    int len, tile, nt, last;        // last: of the block's run
+    int64_t place;                  // in the deal
 };
 
 struct Split {              // a unit whose parts lie in blocks [c0, c1]
@@ -198,20 +199,21 @@ __device__ __forceinline__ int64_t block_scan(int64_t x, bool small, int64_t *s,
     return x;
 }
 
-// Wait for a phase of a barrier, about a second at most: then GDN_DEV_TIMEOUT is set, and the
-// warps of the block leave after their next wait (its outputs are invalid).
-__device__ __forceinline__ void wait_phase(uint32_t bar, uint32_t parity, volatile int *abort, int32_t *status)
+// Wait for a phase of a barrier, about a second at most: then GDN_DEV_TIMEOUT is set and the warps
+// of the block leave at their next wait that has to wait (its outputs are invalid).  Whether the
+// phase came, for the whole warp.
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile int *abort, int32_t *status)
 {
-    if (sm100::mbar_try_wait(bar, parity)) return;
-    const long long start = clock64();
-    while (!sm100::mbar_try_wait(bar, parity)) {
-        if (*abort) return;
-        if (clock64() - start > (1ll << 31)) {
-            *abort = 1;
-            if (status) atomicOr(status, GDN_DEV_TIMEOUT);
-            return;
-        }
+    bool came = sm100::mbar_try_wait(bar, parity);
+    if (!came) {
+        const long long start = clock64();
+        while (!(came = sm100::mbar_try_wait(bar, parity)) && !*abort)
+            if (clock64() - start > (1ll << 31)) {
+                *abort = 1;
+                if (status) atomicOr(status, GDN_DEV_TIMEOUT);
+            }
     }
+    return __all_sync(0xffffffffu, came);
 }
 
 template <bool BF16>
@@ -361,8 +363,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                 const int pg = (int)((uint32_t)j / (uint32_t)kv.page_size);
                 page[w] = j < len && in_range(pg, 1, kv.width, a.dev_status) ? __ldg(row + pg) : -1;
             }
-            if (i >= kStages) wait_phase(empty0 + 8 * st, ((i / kStages) & 1) ^ 1, &s_abort, a.dev_status);
-            if (__any_sync(0xffffffffu, s_abort)) break;
+            if (i >= kStages && !wait_phase(empty0 + 8 * st, ((i / kStages) & 1) ^ 1, &s_abort, a.dev_status)) break;
             int boxes = 0;
 #pragma unroll
             for (int w = 0; w < C::FW; ++w) {
@@ -377,7 +378,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             if (lane == 0) {
                 if (fw == 0) {
                     Desc d;
-                    d.b = cb; d.u = cu; d.base = base; d.len = len; d.tile = ct; d.nt = cnt - kUnitCost;
+                    d.b = cb; d.h = h; d.rt = cu - h * RT; d.base = base; d.len = len; d.tile = ct; d.nt = cnt - kUnitCost;
                     d.last = !more; d.place = place;
                     s_desc[st] = d;
                 }
@@ -452,10 +453,11 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     const uint32_t meet = smem_u32(&s_meet);
     uint32_t met = 0;       // parity of the next meeting
     // all four warps are here (or, after a timeout, need not be)
+    bool together = true;
     auto meet_all = [&]() {
         __syncwarp();
         if (lane == 0) sm100::mbar_arrive(meet);
-        wait_phase(meet, met, &s_abort, a.dev_status);
+        together = wait_phase(meet, met, &s_abort, a.dev_status) && together;
         met ^= 1;
     };
     const int tq = lane & 3, lr = lane >> 2;
@@ -470,10 +472,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
 #pragma unroll 1
     for (int i = 0;; ++i) {
         const int st = i % kStages;
-        wait_phase(full0 + 8 * st, (i / kStages) & 1, &s_abort, a.dev_status);
-        if (__any_sync(0xffffffffu, s_abort)) break;
+        if (!wait_phase(full0 + 8 * st, (i / kStages) & 1, &s_abort, a.dev_status)) break;
         const Desc d = s_desc[st];
-        const int h = d.u / RT, rt = d.u - h * RT;
+        const int h = d.h, rt = d.rt;
 
         if (i == 0 || d.tile == 0) {        // a unit begins: its query rows
             seg_tile = d.tile;
@@ -817,7 +818,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                     meet_all();
                 }
             }
-            if (__any_sync(0xffffffffu, s_abort)) break;
+            if (!together) break;
             const bool whole = seg_tile == 0 && d.tile == d.nt - 1;
             if (wt == 0) {
 #pragma unroll
@@ -852,13 +853,14 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             }
             // the block where a unit begins says who holds its parts
             if (tid == 0 && seg_tile == 0) {
-                const int64_t unit = (int64_t)d.b * U + d.u;
+                const int u = h * RT + rt;
+                const int64_t unit = (int64_t)d.b * U + u;
                 const int64_t end = d.place + (d.nt - 1 - d.tile);   // the unit's last tile
                 const int last = deal.owner(end);
                 const int64_t at = by_unit ? unit : c;
                 if ((by_unit || !whole) && in_range(at, 1, n_splits, a.dev_status)) {
                     Split sp;
-                    sp.u_lo = d.u; sp.b = d.b; sp.c0 = c; sp.c1 = whole ? -1 : last;
+                    sp.u_lo = u; sp.b = d.b; sp.c0 = c; sp.c1 = whole ? -1 : last;
                     splits[at] = sp;
                 }
             }
