@@ -78,6 +78,12 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// bring the line that holds p into L1 (a load that nobody waits for)
+__device__ __forceinline__ void touch_l1(const void *p)
+{
+    asm volatile("{\n\t.reg .b32 x;\n\tld.global.nc.b32 x, [%0];\n\t}" ::"l"(p));
+}
+
 // four e4m3 numbers -> halves (every e4m3 number is one)
 __device__ __forceinline__ void e4m3x4_to_f16x2(uint32_t w, uint32_t &lo, uint32_t &hi)
 {

@@ -269,6 +269,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     __shared__ uint32_t s_valid[kStages][TILE / 32];
     __shared__ float4 s_stat[2][32];
     __shared__ __align__(8) uint64_t s_meet;    // of the warps that compute
+    __shared__ __align__(8) uint64_t s_read;    // a unit's joining has been read
     __shared__ volatile int s_abort;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -287,6 +288,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             sm100::mbar_init(empty0 + 8 * s, kConsumers / 32);
         }
         sm100::mbar_init(smem_u32(&s_meet), kConsumers / 32);
+        sm100::mbar_init(smem_u32(&s_read), WR * C::WD);
         sm100::fence_mbar_init();
         sm100::prefetch_tmap(&kmap);
         sm100::prefetch_tmap(&vmap);
@@ -399,6 +401,16 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                         tma_load_4d(vs + k * TILE * 128 + to, &vmap, full0 + 8 * st, k * 128 / C::ESZ, at, h, page[w]);
                     }
                 }
+            // a unit's query rows are brought near while its first tile is on the way
+            if (i == 0 || ct == 0) {
+                const int r0 = (cu - h * RT) * C::RMAX, lines = (D * 2 + 127) / 128;
+                const int n = min(C::RMAX, rows_all - r0) * lines;
+                for (int k = fw * 32 + lane; k < n; k += C::FETCH * 32) {
+                    const int r = r0 + k / lines, t = r / group;
+                    touch_l1(static_cast<const uint16_t *>(a.q) + ((int64_t)cb * a.T + t) * a.q_token_stride +
+                             (int64_t)(h * group + r - t * group) * a.q_head_stride + (k % lines) * 64);
+                }
+            }
             // the next place of the run (past the last one the cursor may stand anywhere)
             ++place;
             if (++cp == cnt) {
@@ -469,6 +481,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     float xs[E];                            // what a raw score is multiplied by
     int hi[E], lo[E];                       // a row sees lo < j <= hi
     int seg_tile = 0;                       // where the unit's part in this block began
+    int units = 0;                          // done
 #pragma unroll 1
     for (int i = 0;; ++i) {
         const int st = i % kStages;
@@ -500,51 +513,72 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             for (int n = 0; n < C::DW / 8; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
+            // (rows 8 to 15 of a warp, where the unit has none, cost nothing but zeros)
+            const bool two = rows_all - rt * C::RMAX - wr * 16 > 8;
             if constexpr (KIND != kE4M3) {
 #pragma unroll
-                for (int k = 0; k < DP / 16; ++k)
+                for (int e = 0; e < 2; ++e) {
+                    if (e == 0 || two) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int dd = k * 16 + (e >> 1) * 8 + 2 * tq;
-                        qf[k][e] = has[e & 1] && dd < D ? __ldg(qr[e & 1] + dd / 2) : 0u;
+                        for (int k = 0; k < DP / 8; ++k) {
+                            const int dd = k * 8 + 2 * tq;
+                            qf[k / 2][e + 2 * (k & 1)] = has[e] && dd < D ? __ldg(qr[e] + dd / 2) : 0u;
+                        }
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < DP / 8; ++k) qf[k / 2][e + 2 * (k & 1)] = 0u;
                     }
+                }
             } else {
                 // Rows of q become halves, scaled by the power of two that brings the largest
                 // element to [2^7, 2^8): a bf16 or fp16 number down to 2^-22 of it is kept
                 // exactly, smaller ones to 2^-33 of it.  The order of the dimensions is that of
                 // the keys' 16-byte pieces: thread tq of a quad has 16 of each 64 in a row.
-                auto value = [&](uint32_t x, int half) {
-                    const uint16_t v = (uint16_t)(half ? x >> 16 : x & 0xffffu);
-                    return a.q_bf16 ? __uint_as_float((uint32_t)v << 16) : __half2float(__ushort_as_half(v));
-                };
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    auto pair = [&](int s, int k) {
-                        const int dd = s * 64 + tq * 16 + 2 * k;
-                        return has[e] && dd < D ? __ldg(qr[e] + dd / 2) : 0u;
+                auto load = [&](auto bf16) {
+                    auto value = [&](uint32_t x, int half) {
+                        if constexpr (decltype(bf16)::value)
+                            return __uint_as_float(half ? x & 0xffff0000u : x << 16);
+                        else
+                            return __half2float(__ushort_as_half((unsigned short)(half ? x >> 16 : x & 0xffffu)));
                     };
-                    // two passes over the row, so that it need not be held twice
-                    float top = 0.f;
 #pragma unroll
-                    for (int s = 0; s < DP / 64; ++s)
+                    for (int e = 0; e < 2; ++e) {
+                        if (e == 1 && !two) {
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const uint32_t w = pair(s, k);
-                            top = fmaxf(top, fmaxf(fabsf(value(w, 0)), fabsf(value(w, 1))));
+                            for (int k = 0; k < DP / 8; ++k) qf[k / 2][e + 2 * (k & 1)] = 0u;
+                            break;
                         }
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                    const int ex = min(max((int)(__float_as_uint(top) >> 23), 8), 254);
-                    const float up = __uint_as_float((uint32_t)(261 - ex) << 23);
-                    xs[e] = x2 * __uint_as_float((uint32_t)(ex - 7) << 23);
+                        auto pair = [&](int s, int k) {
+                            const int dd = s * 64 + tq * 16 + 2 * k;
+                            return has[e] && dd < D ? __ldg(qr[e] + dd / 2) : 0u;
+                        };
+                        // two passes over the row, so that it need not be held twice
+                        float top = 0.f;
 #pragma unroll
-                    for (int s = 0; s < DP / 64; ++s)
+                        for (int s = 0; s < DP / 64; ++s)
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const uint32_t w = pair(s, k);
-                            qf[s * 4 + k / 2][e + 2 * (k & 1)] = pack_f16x2(value(w, 0) * up, value(w, 1) * up);
-                        }
-                }
+                            for (int k = 0; k < 8; ++k) {
+                                const uint32_t w = pair(s, k);
+                                top = fmaxf(top, fmaxf(fabsf(value(w, 0)), fabsf(value(w, 1))));
+                            }
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                        const int ex = min(max((int)(__float_as_uint(top) >> 23), 8), 254);
+                        const float up = __uint_as_float((uint32_t)(261 - ex) << 23);
+                        xs[e] = x2 * __uint_as_float((uint32_t)(ex - 7) << 23);
+#pragma unroll
+                        for (int s = 0; s < DP / 64; ++s)
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                const uint32_t w = pair(s, k);
+                                qf[s * 4 + k / 2][e + 2 * (k & 1)] = pack_f16x2(value(w, 0) * up, value(w, 1) * up);
+                            }
+                    }
+                };
+                if (a.q_bf16)
+                    load(std::true_type{});
+                else
+                    load(std::false_type{});
             }
         }
 
@@ -773,51 +807,62 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                     for (int k = 0; k < 4; ++k) o[n][k] *= vsc;
             }
             // The other warps of the same rows and dimensions join into wt = 0, halving their
-            // number; rows 8 to 15 only where the unit has them (one or two writers of 4 KB).
+            // number; rows 8 to 15 only where the unit has them.  A writer's 4 KB are those that it
+            // has just read itself, or of the unit before, whose last reader says so (s_read).
             constexpr int kQ = C::DW / 16;              // float4 of a row's
+            const int halves = rows_all - rt * C::RMAX > 8 ? 2 : 1;
             const bool two = rows_all - rt * C::RMAX - wr * 16 > 8;
+            if (C::WT > 1 && wt > 0)
+                together = wait_phase(smem_u32(&s_read), units & 1 ^ 1, &s_abort, a.dev_status) && together;
+            float fj[2][2][2];      // weights of the two parts, by step and row
 #pragma unroll
-            for (int half = C::WT / 2; half > 0; half >>= 1) {
-                float4 *const buf = s_merge + (warp % (half * WR * C::WD)) * kQ * 32 + lane;
-                float f0[2], f1[2];
+            for (int e = 0; e < 2; ++e) {
+                if (C::WT == 1 || e >= halves) break;
+                if (e == 1) meet_all();             // the first halves have been read
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    if (e == 1 && rows_all - rt * C::RMAX <= 8) break;
-                    if (wt >= half && wt < 2 * half) {
-                        if (e == 0) s_stat[warp % (half * WR * C::WD)][lane] = make_float4(m[0], m[1], l[0], l[1]);
-                        if (e == 0 || two)
+                for (int half = C::WT / 2; half > 0; half >>= 1) {
+                    // four warps: 2 and 3 write places 0 and 1 for 0 and 1, then 1 writes place 1 for 0
+                    const int at = C::WT == 4 && half == 1 ? 1 : warp % (half * WR * C::WD);
+                    float4 *const buf = s_merge + at * kQ * 32 + lane;
+                    float4 *const stat = &s_stat[at][lane];
+                    float(&f)[2][2] = fj[half / 2];
+                    if (wt >= half && wt < 2 * half && (e == 0 || two)) {
+                        if (e == 0) *stat = make_float4(m[0], m[1], l[0], l[1]);
 #pragma unroll
-                            for (int k = 0; k < kQ; ++k)
-                                buf[k * 32] = make_float4(o[2 * k][2 * e], o[2 * k][2 * e + 1],
-                                                          o[2 * k + 1][2 * e], o[2 * k + 1][2 * e + 1]);
+                        for (int k = 0; k < kQ; ++k)
+                            buf[k * 32] = make_float4(o[2 * k][2 * e], o[2 * k][2 * e + 1], o[2 * k + 1][2 * e],
+                                                      o[2 * k + 1][2 * e + 1]);
                     }
                     meet_all();
-                    if (wt < half) {
+                    if (wt < half && (e == 0 || two)) {
                         if (e == 0) {
-                            const float4 y = s_stat[warp % (half * WR * C::WD)][lane];
+                            const float4 y = *stat;
 #pragma unroll
                             for (int r = 0; r < 2; ++r) {
                                 const float ym = r ? y.y : y.x, yl = r ? y.w : y.z;
                                 const float mx = fmaxf(m[r], ym), ms = mx == -INFINITY ? 0.f : mx;
-                                f0[r] = ex2_approx(m[r] - ms);
-                                f1[r] = ex2_approx(ym - ms);
+                                f[r][0] = ex2_approx(m[r] - ms);
+                                f[r][1] = ex2_approx(ym - ms);
                                 m[r] = mx;
-                                l[r] = l[r] * f0[r] + yl * f1[r];
+                                l[r] = l[r] * f[r][0] + yl * f[r][1];
                             }
                         }
-                        if (e == 0 || two)
 #pragma unroll
-                            for (int k = 0; k < kQ; ++k) {
-                                const float4 y = buf[k * 32];
-                                o[2 * k][2 * e] = o[2 * k][2 * e] * f0[e] + y.x * f1[e];
-                                o[2 * k][2 * e + 1] = o[2 * k][2 * e + 1] * f0[e] + y.y * f1[e];
-                                o[2 * k + 1][2 * e] = o[2 * k + 1][2 * e] * f0[e] + y.z * f1[e];
-                                o[2 * k + 1][2 * e + 1] = o[2 * k + 1][2 * e + 1] * f0[e] + y.w * f1[e];
-                            }
+                        for (int k = 0; k < kQ; ++k) {
+                            const float4 y = buf[k * 32];
+                            o[2 * k][2 * e] = o[2 * k][2 * e] * f[e][0] + y.x * f[e][1];
+                            o[2 * k][2 * e + 1] = o[2 * k][2 * e + 1] * f[e][0] + y.y * f[e][1];
+                            o[2 * k + 1][2 * e] = o[2 * k + 1][2 * e] * f[e][0] + y.z * f[e][1];
+                            o[2 * k + 1][2 * e + 1] = o[2 * k + 1][2 * e + 1] * f[e][0] + y.w * f[e][1];
+                        }
                     }
-                    meet_all();
                 }
             }
+            if (C::WT > 1 && wt == 0) {
+                __syncwarp();
+                if (lane == 0) sm100::mbar_arrive(smem_u32(&s_read));
+            }
+            ++units;
             if (!together) break;
             const bool whole = seg_tile == 0 && d.tile == d.nt - 1;
             if (wt == 0) {
