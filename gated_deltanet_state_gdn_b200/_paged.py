@@ -9,6 +9,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import math
+import struct
 
 import torch
 
@@ -36,6 +37,12 @@ class _Table(ctypes.Structure):
                 ("seq_lens", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
                 ("rows", ctypes.c_int32), ("width", ctypes.c_int32),
                 ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32)]
+
+
+# the bytes of the two, packed at once: filling a ctypes structure field by field would be a tenth
+# of a small call's host time
+_CACHE_BYTES = struct.Struct("@PPqqqPPPPqiiiiiii4x")
+_TABLE_BYTES = struct.Struct("@PPPqiiii")
 
 
 class _Pool(ctypes.Structure):
@@ -72,6 +79,10 @@ def _stream(device):
 
 def _at(t):
     return None if t is None else t.data_ptr()
+
+
+def _here(t):
+    return 0 if t is None else t.data_ptr()
 
 
 @functools.lru_cache(maxsize=256)
@@ -112,6 +123,7 @@ def _rows_of(block_table, device):
 
 
 def _cache(k_cache, v_cache, block_table, seq_lens, k_scale, v_scale):
+    """The bytes of the call's gdn_paged_cache; its heads, head_dim, dtype code and rows."""
     dtype, device = k_cache.dtype, k_cache.device
     code = _CACHE_DTYPES.get(dtype)
     if code is None:
@@ -131,9 +143,9 @@ def _cache(k_cache, v_cache, block_table, seq_lens, k_scale, v_scale):
         _tensor("k_scale", k_scale, torch.float32, (H,), device)
     if v_scale is not None:
         _tensor("v_scale", v_scale, torch.float32, (H,), device)
-    return _Cache(k_cache.data_ptr(), v_cache.data_ptr(), st[0], st[1], st[2],
-                  _at(k_scale), _at(v_scale), block_table.data_ptr(),
-                  seq_lens.data_ptr(), stride, rows, width, P, S, H, D, code)
+    return _CACHE_BYTES.pack(k_cache.data_ptr(), v_cache.data_ptr(), st[0], st[1], st[2],
+                             _here(k_scale), _here(v_scale), block_table.data_ptr(),
+                             seq_lens.data_ptr(), stride, rows, width, P, S, H, D, code), H, D, code, rows
 
 
 def _row_strides(name, t, heads, D, unit):
@@ -180,23 +192,23 @@ def gdn_kv_append(k, v, k_cache, v_cache, block_table, seq_lens, slots=None, row
     dt = _DTYPES.get(k.dtype)
     if dt is None:
         raise TypeError(f"k must be bf16 or fp16, got {k.dtype}")
-    cache = _cache(k_cache, v_cache, block_table, seq_lens, k_scale, v_scale)
+    cache, heads, D, _, rows = _cache(k_cache, v_cache, block_table, seq_lens, k_scale, v_scale)
     device = k.device
     if k_cache.device != device:
         raise TypeError(f"k_cache must be on {device}")
     _tensor("v", v, k.dtype, k.shape, device, dense=False)
-    k, kt, kh = _row_strides("k", k, cache.heads, cache.head_dim, 8)
-    v, vt, vh = _row_strides("v", v, cache.heads, cache.head_dim, 8)
+    k, kt, kh = _row_strides("k", k, heads, D, 8)
+    v, vt, vh = _row_strides("v", v, heads, D, 8)
     N = math.prod(k.shape[:-2])
     if slots is not None:
         B = slots.shape[0]
     elif row_offsets is not None:
         B = row_offsets.shape[0] - 1
     else:
-        B = k.shape[0] if k.dim() == 4 else cache.rows
+        B = k.shape[0] if k.dim() == 4 else rows
     slots = _ints("slots", slots, B, device)
     row_offsets = _ints("row_offsets", row_offsets, B + 1, device)
-    _raise(b.lib().gdn_kv_append(_at(k), _at(v), kt, kh, vt, vh, ctypes.byref(cache),
+    _raise(b.lib().gdn_kv_append(_at(k), _at(v), kt, kh, vt, vh, cache,
                                  _at(slots), _at(row_offsets), B, N, dt,
                                  _at(dev_status), _stream(device)), "gdn_kv_append")
     return k_cache, v_cache
@@ -224,8 +236,8 @@ def gdn_paged_attn(q, k_cache, v_cache, block_table, seq_lens, slots=None, *, sc
     device = q.device
     if k_cache.device != device:
         raise TypeError(f"k_cache must be on {device}")
-    cache = _cache(k_cache, v_cache, block_table, seq_lens, k_scale, v_scale)
-    q, qt, qh = _row_strides("q", q, 0, cache.head_dim, 2)
+    cache, heads, cache_dim, code, _ = _cache(k_cache, v_cache, block_table, seq_lens, k_scale, v_scale)
+    q, qt, qh = _row_strides("q", q, 0, cache_dim, 2)
     slots = _ints("slots", slots, B, device)
     flags = 0
     if (out is None) != (lse is None) and (out is not None or return_lse):
@@ -235,7 +247,7 @@ def gdn_paged_attn(q, k_cache, v_cache, block_table, seq_lens, slots=None, *, sc
         else:
             lse = torch.full((B, T, Hq), -math.inf, device=device) if return_lse else None
     if out is None:
-        out = q.new_empty((B, T, Hq, D))
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
         flags = b.GDN_ZERO_PADDING
     else:
         _tensor("out", out, q.dtype, (B, T, Hq, D), device)
@@ -244,9 +256,9 @@ def gdn_paged_attn(q, k_cache, v_cache, block_table, seq_lens, slots=None, *, sc
     elif return_lse:
         lse = q.new_empty((B, T, Hq), dtype=torch.float32)
     L = b.lib()
-    nbytes = _attn_workspace(L, device, B, T, Hq, cache.heads, cache.head_dim, cache.dtype)
+    nbytes = _attn_workspace(L, device, B, T, Hq, heads, D, code)
     ws = q.new_empty((max(nbytes, 16),), dtype=torch.uint8)
-    _raise(L.gdn_paged_attn(_at(q), qt, qh, ctypes.byref(cache), _at(slots), B, T, Hq, dt,
+    _raise(L.gdn_paged_attn(_at(q), qt, qh, cache, _at(slots), B, T, Hq, dt,
                             1.0 / math.sqrt(D) if scale is None else float(scale), int(window),
                             _at(out), _at(lse), flags, _at(ws), nbytes,
                             _at(dev_status), _stream(device)), "gdn_paged_attn")
@@ -254,19 +266,25 @@ def gdn_paged_attn(q, k_cache, v_cache, block_table, seq_lens, slots=None, *, sc
 
 
 def _table(block_table, ref_count, seq_lens, page_size):
+    """The bytes of the call's gdn_page_table; its rows and pages."""
     device = block_table.device
     rows, width, stride = _rows_of(block_table, device)
     _tensor("seq_lens", seq_lens, _I32, (rows,), device)
-    _tensor("ref_count", ref_count, _I32, (ref_count.numel(),), device)
-    return _Table(block_table.data_ptr(), ref_count.data_ptr(), seq_lens.data_ptr(), stride,
-                  rows, width, ref_count.shape[0], int(page_size))
+    if not isinstance(ref_count, torch.Tensor) or ref_count.dim() != 1:
+        raise TypeError(f"ref_count must be a 1-d int32 tensor on {device}")
+    pages = ref_count.shape[0]
+    _tensor("ref_count", ref_count, _I32, (pages,), device)
+    return _TABLE_BYTES.pack(block_table.data_ptr(), ref_count.data_ptr(), seq_lens.data_ptr(), stride,
+                             rows, width, pages, int(page_size)), rows, pages
 
 
 def _pools(pools, rows, device):
     """The arrays of a call: dimension 0 counts pages (or slots), the others are one dense block."""
     if isinstance(pools, torch.Tensor):
         raise TypeError("pools must be a list of tensors")
-    out = (_Pool * max(len(pools), 1))()
+    if not pools:
+        return None, 0
+    out = (_Pool * len(pools))()
     for i, t in enumerate(pools):
         if not isinstance(t, torch.Tensor) or t.device != device or t.dim() < 1:
             raise TypeError(f"pools[{i}] must be a tensor on {device}")
@@ -297,15 +315,15 @@ def gdn_page_resize(block_table, ref_count, seq_lens, row_list, new_lens, page_s
     Returns (block_table, ref_count, seq_lens).
     """
     device = block_table.device
-    t = _table(block_table, ref_count, seq_lens, page_size)
+    t, rows, num_pages = _table(block_table, ref_count, seq_lens, page_size)
     n = row_list.shape[0]
     row_list = _ints("row_list", row_list, n, device)
     new_lens = _ints("new_lens", new_lens, n, device)
-    arr, count = _pools(pools, t.num_pages, device)
+    arr, count = _pools(pools, num_pages, device)
     L = b.lib()
-    nbytes = L.gdn_page_workspace_size(t.num_pages, max(n, 1))
+    nbytes = L.gdn_page_workspace_size(num_pages, max(n, 1))
     ws = block_table.new_empty((nbytes,), dtype=torch.uint8)
-    _raise(L.gdn_page_resize(ctypes.byref(t), _at(row_list), _at(new_lens), n, arr, count,
+    _raise(L.gdn_page_resize(t, _at(row_list), _at(new_lens), n, arr, count,
                              _at(ws), nbytes, _at(dev_status), _stream(device)),
            "gdn_page_resize")
     return block_table, ref_count, seq_lens
@@ -322,12 +340,12 @@ def gdn_page_fork(block_table, ref_count, seq_lens, parents, children, page_size
     given back.  Returns (block_table, ref_count, seq_lens).
     """
     device = block_table.device
-    t = _table(block_table, ref_count, seq_lens, page_size)
+    t, rows, num_pages = _table(block_table, ref_count, seq_lens, page_size)
     n = parents.shape[0]
     parents = _ints("parents", parents, n, device)
     children = _ints("children", children, n, device)
-    arr, count = _pools(pools, t.rows, device)
-    _raise(b.lib().gdn_page_fork(ctypes.byref(t), _at(parents), _at(children), n, arr,
+    arr, count = _pools(pools, rows, device)
+    _raise(b.lib().gdn_page_fork(t, _at(parents), _at(children), n, arr,
                                  count, _at(dev_status), _stream(device)), "gdn_page_fork")
     return block_table, ref_count, seq_lens
 
@@ -341,15 +359,15 @@ def gdn_page_compact(block_table, ref_count, seq_lens, page_size: int, pools=(),
     int32: the new number of each used page, -1 for free ones.
     """
     device = block_table.device
-    t = _table(block_table, ref_count, seq_lens, page_size)
-    arr, count = _pools(pools, t.num_pages, device)
+    t, rows, num_pages = _table(block_table, ref_count, seq_lens, page_size)
+    arr, count = _pools(pools, num_pages, device)
     if page_map is None:
-        page_map = block_table.new_empty((t.num_pages,))
+        page_map = block_table.new_empty((num_pages,))
     else:
-        _tensor("page_map", page_map, _I32, (t.num_pages,), device)
+        _tensor("page_map", page_map, _I32, (num_pages,), device)
     L = b.lib()
-    nbytes = L.gdn_page_workspace_size(t.num_pages, 0)
+    nbytes = L.gdn_page_workspace_size(num_pages, 0)
     ws = block_table.new_empty((nbytes,), dtype=torch.uint8)
-    _raise(L.gdn_page_compact(ctypes.byref(t), _at(page_map), arr, count, _at(ws), nbytes,
+    _raise(L.gdn_page_compact(t, _at(page_map), arr, count, _at(ws), nbytes,
                               _at(dev_status), _stream(device)), "gdn_page_compact")
     return page_map

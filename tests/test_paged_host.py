@@ -185,6 +185,15 @@ def test_binding_takes_gpu_tensors_only(g):
         g.gdn_page_compact(t, t[0], t[0], 16)
 
 
+def test_packed_structures():
+    """The bytes that the binding packs are the structures that the header declares."""
+    from gated_deltanet_state_gdn_b200 import _paged as p
+    for cls, packed in ((p._Cache, p._CACHE_BYTES), (p._Table, p._TABLE_BYTES)):
+        assert ctypes.sizeof(cls) == packed.size
+        values = [1000 + 7 * i for i in range(len(cls._fields_))]
+        assert bytes(cls(*values)) == packed.pack(*values)
+
+
 def test_row_strides():
     """What the binding takes for evenly spaced tokens, and what it copies."""
     from gated_deltanet_state_gdn_b200._paged import _row_strides
