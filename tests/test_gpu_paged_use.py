@@ -153,6 +153,78 @@ def test_given_stream_orders_the_call(gdn):
     assert same(got, want) and same(got2, want)
 
 
+def test_captured_tables_replay(gdn):
+    """A fork, a growth into shared pages and a compaction, captured together."""
+    a, b = Server(11), Server(11)
+    states = [torch.randn(6, 4, 33, device="cuda") for _ in range(2)]
+    states[1].copy_(states[0])
+
+    def turn(s, state):
+        gdn.gdn_page_fork(s.table, s.ref, s.seq, ints_[0], ints_[1], s.page, [state], dev_status=s.status)
+        gdn.gdn_page_resize(s.table, s.ref, s.seq, s.rows, s.lens, s.page, [s.k, s.v], dev_status=s.status)
+        return gdn.gdn_page_compact(s.table, s.ref, s.seq, s.page, [s.k, s.v], dev_status=s.status)
+
+    ints_ = ints([2, 2, 5]), ints([0, 4, 1])
+    for s in (a, b):
+        s.start(gdn)
+    for s, state in zip((a, b), states):
+        turn(s, state)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        to = turn(a, states[0])
+    for n in range(4):
+        for s in (a, b):
+            s.lens.copy_(ints([9 + n, 70, 33 + 2 * n, 5, 64 - 7 * n, 90]))
+        states[0][n] += 1
+        states[1][n] += 1
+        graph.replay()
+        want = turn(b, states[1])
+        torch.cuda.synchronize()
+        assert same(a.everything(), b.everything()) and torch.equal(states[0], states[1])
+        assert torch.equal(to, want)
+    assert int(a.status.item()) == 0
+
+
+def test_views_of_larger_tensors(gdn):
+    """Keys and values of one tensor, heads cut out of it, a table that is part of a wider one."""
+    a, b = Server(12), Server(12)
+    kv = torch.zeros(b.P, 2, b.page, 5, b.D, dtype=torch.bfloat16, device="cuda")
+    kv[:, 0, :, 1:3], kv[:, 1, :, 1:3] = b.k, b.v
+    b.k, b.v = kv[:, 0, :, 1:3], kv[:, 1, :, 1:3]
+    wide = torch.full((6, 33), -9, dtype=torch.int32, device="cuda")
+    wide[:, 4:24] = b.table
+    b.table = wide[:, 4:24]
+    pages = [kv[:, 0], kv[:, 1]]
+    for s, pools in ((a, [a.k, a.v]), (b, pages)):
+        gdn.gdn_page_resize(s.table, s.ref, s.seq, s.rows, s.lens, s.page, pools)
+        gdn.gdn_page_fork(s.table, s.ref, s.seq, ints([5]), ints([3]), s.page)
+        s.lens[3] = 90
+        advance(s, 2)
+        gdn.gdn_page_resize(s.table, s.ref, s.seq, s.rows, s.lens, s.page, pools)
+        gdn.gdn_kv_append(s.kn, s.vn, s.k, s.v, s.table, s.seq, s.slots)
+        gdn.gdn_paged_attn(s.q, s.k, s.v, s.table, s.seq, s.slots, out=s.out)
+        gdn.gdn_page_compact(s.table, s.ref, s.seq, s.page, pools)
+    assert same(a.everything(), b.everything())
+    assert (kv[:, :, :, 0] == 0).all() and (kv[:, :, :, 3:] == 0).all()
+    assert (wide[:, :4] == -9).all() and (wide[:, 24:] == -9).all()
+
+
+@pytest.mark.parametrize("D,cache", [(8, torch.bfloat16), (16, E4M3), (256, torch.float16)])
+def test_smallest_cache(gdn, D, cache):
+    """One page of one token of one head."""
+    dtype = torch.float16 if cache == torch.float16 else torch.bfloat16
+    k, v = (torch.zeros(1, 1, 1, D, device="cuda").to(cache) for _ in range(2))
+    table, seq = ints([[0]]), ints([1])
+    kn = torch.randn(1, 1, 1, D, device="cuda").to(dtype)
+    gdn.gdn_kv_append(kn, -kn, k, v, table, seq)
+    assert torch.equal(k.float(), kn.to(cache).float()) and torch.equal(v.float(), (-kn).to(cache).float())
+    out, lse = gdn.gdn_paged_attn(kn, k, v, table, seq, return_lse=True)
+    assert torch.equal(out.float(), v.float().to(dtype).float())
+    x = (kn.double() * k.double()).sum() / D ** 0.5
+    assert abs(float(lse) - float(x)) <= (D + 8) * 2.0 ** -22 * float((kn.double() * k.double()).abs().sum())
+
+
 def test_wrong_devices_are_refused(gdn):
     c = Case(4, [5])
     args = [c.to(x) for x in (c.q, c.k, c.v, c.table, c.seq, c.slots)]

@@ -187,6 +187,17 @@ def test_many_rows_and_pages(gdn):
     assert s.model.status == 0
 
 
+def test_many_children(gdn):
+    s = State(1800, 4, 300, 4, pools=1, slots=1, seed=3)
+    s.resize(gdn, [7, 9], [13, 6])
+    s.fork(gdn, [7] * 900 + [9] * 800, list(range(10, 910)) + list(range(950, 1750)))
+    # a copy of the shared last page for each: 290 of the 300 - 4 - 2 free pages
+    s.resize(gdn, list(range(10, 300)), [14] * 290)
+    assert s.model.status == 0
+    s.resize(gdn, list(range(300, 310)), [14] * 10)       # four are left
+    assert s.model.status == gdn.GDN_DEV_NO_PAGES
+
+
 def test_more_asked_for_than_32_bits_count(gdn):
     """2200 rows that ask for a million pages each: more than 2^31 in all, of a hundred there are.
     The row ahead of them fits; the ones behind the shortage wait, however little they ask for."""
