@@ -599,16 +599,26 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             // scores of the rows and STEP tokens
             float x[NX][4] = {};
             if constexpr (KIND != kE4M3) {
+                // four chains of products: two blocks of 16 tokens, or even and odd steps of one
                 const int r = tok + (lane & 7) + ((lane >> 4) << 3);
+                float y[NX][4] = {};
 #pragma unroll
                 for (int k = 0; k < DP / 16; ++k)
 #pragma unroll
                     for (int u = 0; u < NX / 2; ++u) {
                         uint32_t b[4];
                         ldmatrix_x4(b, ks + piece<C>(r + 16 * u, 2 * k + ((lane >> 3) & 1)));
-                        mma_16816<BF16>(x[2 * u], qf[k][0], qf[k][1], qf[k][2], qf[k][3], b[0], b[1]);
-                        mma_16816<BF16>(x[2 * u + 1], qf[k][0], qf[k][1], qf[k][2], qf[k][3], b[2], b[3]);
+                        float(&x0)[4] = NX == 2 && (k & 1) ? y[0] : x[2 * u];
+                        float(&x1)[4] = NX == 2 && (k & 1) ? y[1] : x[2 * u + 1];
+                        mma_16816<BF16>(x0, qf[k][0], qf[k][1], qf[k][2], qf[k][3], b[0], b[1]);
+                        mma_16816<BF16>(x1, qf[k][0], qf[k][1], qf[k][2], qf[k][3], b[2], b[3]);
                     }
+                if constexpr (NX == 2) {
+#pragma unroll
+                    for (int n = 0; n < 2; ++n)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) x[n][k] += y[n][k];
+                }
             } else {
 #pragma unroll
                 for (int q4 = 0; q4 < DP / 64; ++q4) {
