@@ -21,8 +21,10 @@ using gdn::in_range;
 constexpr int kCluster = 16;            // planning blocks at most
 constexpr int kThreads = 1024;          // of one
 constexpr int kChunk = 256;             // table entries a warp takes at a time
-constexpr int kPer = 16;                // pages a thread takes at a time
+constexpr int kPer = 16;                // pages a thread takes at a time at most, 32 apart
 constexpr int kNear = 1024;             // listed rows whose plan is kept in shared memory
+constexpr int kSlots = 4096;            // of the table that finds rows listed twice
+constexpr int kHashed = 3072;           // listed rows that it is used for
 constexpr int kCopyThreads = 256;
 constexpr int kCopyBytes = 16384;       // of a row a block copies at a time
 constexpr int kMaxPools = 96;           // a launch (a kernel's arguments hold 4 KB)
@@ -79,29 +81,45 @@ __device__ __forceinline__ T block_scan(T x, T *s_warp, T *total)
     return before + incl - x;
 }
 
-// Bit k: page p + k (< end) is used (free).  Whole vectors where the counts are aligned.
-__device__ __forceinline__ uint32_t used_pages(const int32_t *ref, int p, int end, bool vec, uint32_t *in)
-{
-    uint32_t used = 0, there = 0;
-    if (vec && p + kPer <= end) {
-        int4 v[kPer / 4];
-#pragma unroll
-        for (int k = 0; k < kPer / 4; ++k) v[k] = __ldcg(reinterpret_cast<const int4 *>(ref + p) + k);
-#pragma unroll
-        for (int k = 0; k < kPer / 4; ++k)
-            used |= ((uint32_t)(v[k].x > 0) | (uint32_t)(v[k].y > 0) << 1 | (uint32_t)(v[k].z > 0) << 2 |
-                     (uint32_t)(v[k].w > 0) << 3) << (4 * k);
-        there = (1u << kPer) - 1;
-    } else {
-#pragma unroll
-        for (int k = 0; k < kPer; ++k)
-            if (p + k < end) {
-                used |= (uint32_t)(__ldcg(ref + p + k) > 0) << k;
-                there |= 1u << k;
-            }
+// Which of the next 32 `per` pages from p on (below end) are used: bit `lane` of word e is page
+// p + 32 e + lane.  A block takes 1024 `per` pages at a time, as few a warp as its share allows.
+struct Used {
+    uint32_t w[kPer];
+    int left;                           // pages there are
+    __device__ __forceinline__ uint32_t in(int e) const
+    {
+        const int n = left - 32 * e;
+        return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1);
     }
-    *in = there;
-    return used;
+    __device__ __forceinline__ uint32_t open(int e) const { return in(e) & ~w[e]; }
+    __device__ __forceinline__ void look(const int32_t *ref, int p, int end, int per)
+    {
+        const int lane = threadIdx.x & 31;
+        left = min(max(end - p, 0), 32 * per);
+        int v[kPer];
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) v[e] = 32 * e + lane < left ? __ldcg(ref + p + 32 * e + lane) : 0;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+            w[e] = 0;
+            if (32 * e < left) w[e] = __ballot_sync(0xffffffffu, v[e] > 0);
+        }
+    }
+    __device__ __forceinline__ int used() const
+    {
+        int n = 0;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e)
+            if (32 * e < left) n += __popc(w[e]);
+        return n;
+    }
+};
+__device__ __forceinline__ int words_of(int pages) { return min(kPer, (pages + kThreads - 1) / kThreads); }
+
+// exclusive prefix sum over the block's warps of a value that a warp's lanes share
+__device__ __forceinline__ int warps_scan(int x, int *s_warp, int *total)
+{
+    return block_scan<int>((threadIdx.x & 31) == 0 ? x : 0, s_warp, total);
 }
 
 // copy piece `item` of row src to row dst
@@ -198,12 +216,14 @@ resize_kernel(const __grid_constant__ gdn_page_table t, const int32_t *row_list,
     const int blocks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     const int tid = threadIdx.x, lane = tid & 31;
     const int warps = blocks * (kThreads / 32), gw = (tid >> 5) * blocks + rank;    // of the cluster
-    __shared__ __align__(16) int s_list[kThreads];
     __shared__ int s_warp[32];
     __shared__ long long s_wide[32];
     __shared__ int s_most[2];
     __shared__ int s_free;
     __shared__ Row s_rows[kNear];
+    static_assert(kSlots * sizeof(int) <= sizeof(s_rows), "the table and the rows share their place");
+    int *const s_key = reinterpret_cast<int *>(s_rows);
+    constexpr int kTwice = (int)0x80000000;     // (-1 is a free slot: no row is 0x7fffffff)
     Row *const rows = n <= kNear ? s_rows : ws.rows + (int64_t)rank * n;
     launch_dependents();
     // the steps' order: among the blocks, or the threads of the only one
@@ -211,33 +231,61 @@ resize_kernel(const __grid_constant__ gdn_page_table t, const int32_t *row_list,
         if (blocks > 1) cluster.sync(); else __syncthreads();
     };
 
-    // 1. what is asked of each row (every block works it out for itself)
+    // 1. what is asked of each row (every block works it out for itself).  Rows listed twice meet in
+    //    a table in shared memory, or, of more than kHashed, are looked for one by one.
     if (tid == 0) s_most[0] = s_most[1] = 0;
+    if (n <= kHashed) {
+        for (int k = tid; k < kSlots; k += kThreads) s_key[k] = -1;
+        __syncthreads();
+        for (int i = tid; i < n; i += kThreads) {
+            const int r = __ldg(row_list + i);
+            if (r < 0 || r >= t.rows) continue;
+            // (at most kHashed rows: a free slot is found)
+            for (uint32_t h = (uint32_t)r * 2654435769u >> 20;; h = (h + 1) % kSlots) {
+                const int was = atomicCAS(s_key + h, -1, r);
+                if (was == r || was == (r | kTwice)) {
+                    s_key[h] = r | kTwice;      // (whoever writes it, writes the same)
+                    break;
+                }
+                if (was == -1) break;
+            }
+        }
+        __syncthreads();
+    }
+    auto listed_twice = [&](int r) {
+        for (uint32_t h = (uint32_t)r * 2654435769u >> 20;; h = (h + 1) % kSlots) {
+            const int k = s_key[h];
+            if (k == r) return false;
+            if (k == (r | kTwice)) return true;
+        }
+    };
     for (int i0 = 0; i0 < n; i0 += kThreads) {
         const int i = i0 + tid;
         const int r = i < n ? __ldg(row_list + i) : -1;
         const bool there = r >= 0 && r < t.rows;
         const int old = there ? __ldcg(t.seq_lens + r) : 0, len = i < n ? __ldg(new_lens + i) : 0;
-        int twice = 0;
-        for (int k0 = 0; k0 < n; k0 += kThreads) {
-            __syncthreads();
-            s_list[tid] = k0 == i0 ? r : (k0 + tid < n ? __ldg(row_list + k0 + tid) : -1);
-            __syncthreads();
-            if (i < n) {
-                const int most = (min(kThreads, n - k0) + 3) / 4;
-                for (int k = 0; k < most; ++k) {
-                    const int4 q = reinterpret_cast<const int4 *>(s_list)[k];
-                    twice += (q.x == r) + (q.y == r) + (q.z == r) + (q.w == r);
+        bool twice = false;
+        if (n <= kHashed) {
+            twice = there && listed_twice(r);
+        } else {
+            int times = 0;
+            for (int k0 = 0; k0 < n; k0 += kSlots) {
+                __syncthreads();
+                for (int k = tid; k < kSlots; k += kThreads) s_key[k] = k0 + k < n ? __ldg(row_list + k0 + k) : -1;
+                __syncthreads();
+                for (int k = 0; k < kSlots / 4 && i < n; ++k) {
+                    const int4 q = reinterpret_cast<const int4 *>(s_key)[k];
+                    times += (q.x == r) + (q.y == r) + (q.z == r) + (q.w == r);
                 }
             }
+            twice = times > 1;
         }
-        if (i >= n) continue;
         Row x = {-1, 0, 0, 0, 0, 0, 0, 0};
         int bad = 0;
         if (r >= t.rows) {
             bad = GDN_DEV_BAD_SLOT;
         } else if (r >= 0) {
-            if (twice > 1) {
+            if (twice) {
                 bad = GDN_DEV_CONFLICT;
             } else if (!length_ok(t, old) || !length_ok(t, len)) {
                 bad = GDN_DEV_BAD_LENGTH;
@@ -252,7 +300,8 @@ resize_kernel(const __grid_constant__ gdn_page_table t, const int32_t *row_list,
             }
         }
         if (bad && rank == 0) tell(status, bad);
-        rows[i] = x;
+        if (n <= kNear) __syncthreads();        // the table has been read: the rows take its place
+        if (i < n) rows[i] = x;
     }
     __syncthreads();
     const int most_gone = s_most[0], most_new = s_most[1];
@@ -320,20 +369,20 @@ resize_kernel(const __grid_constant__ gdn_page_table t, const int32_t *row_list,
     //    are exchanged, then it writes its part of the list
     int free_all = 0;
     if (total > 0) {
-        const bool vec = ((uintptr_t)t.ref_count & 15) == 0;
-        const int share = ((t.num_pages + blocks - 1) / blocks + kPer - 1) / kPer * kPer;
+        const int share = ((t.num_pages + blocks - 1) / blocks + 31) / 32 * 32;
         const int p0 = min(rank * share, t.num_pages), p1 = min(p0 + share, t.num_pages);
-        const bool once = blocks > 1 && share <= kThreads * kPer;   // what is counted need not be read again
-        uint32_t in, open = 0;
+        const int per = words_of(p1 - p0), pass = kThreads * per;
+        const bool once = p1 - p0 <= pass;      // what is counted need not be read again
+        const int warp_at = (tid >> 5) * 32 * per;
+        Used u;
         int at = 0, sum;
         if (blocks > 1) {
             int mine = 0;
-            for (int p = p0 + tid * kPer; p < p1; p += kThreads * kPer) {
-                const uint32_t used = used_pages(t.ref_count, p, p1, vec, &in);
-                open = in & ~used;
-                mine += __popc(open);
+            for (int q = p0; q < p1; q += pass) {
+                u.look(t.ref_count, q + warp_at, p1, per);
+                mine += u.left - u.used();
             }
-            block_scan<int>(mine, s_warp, &sum);
+            warps_scan(mine, s_warp, &sum);
             if (tid == 0) s_free = sum;
             cluster.sync();
             for (int k = 0; k < blocks; ++k) {
@@ -342,15 +391,20 @@ resize_kernel(const __grid_constant__ gdn_page_table t, const int32_t *row_list,
                 free_all += f;
             }
         }
-        for (int q = p0; q < p1 && at < total; q += kThreads * kPer) {
-            const int p = q + tid * kPer;
-            if (!once) {
-                open = ~used_pages(t.ref_count, p, p1, vec, &in);
-                open &= in;
+        for (int q = p0; q < p1 && at < total; q += pass) {
+            const int p = q + warp_at;
+            if (blocks == 1 || !once) u.look(t.ref_count, p, p1, per);
+            int k = at + warps_scan(u.left - u.used(), s_warp, &sum);
+            k = __shfl_sync(0xffffffffu, k, 0);
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) {
+                if (32 * e >= u.left) break;
+                const uint32_t open = u.open(e);
+                const int kk = k + __popc(open & ((1u << lane) - 1));
+                if ((open >> lane & 1) && kk < total && in_range(kk, 1, t.num_pages, status))
+                    ws.free_list[kk] = p + 32 * e + lane;
+                k += __popc(open);
             }
-            int k = at + block_scan<int>(__popc(open), s_warp, &sum);
-            for (; open && k < total; open &= open - 1, ++k)
-                if (in_range(k, 1, t.num_pages, status)) ws.free_list[k] = p + __ffs(open) - 1;
             at += sum;
         }
         if (blocks == 1) free_all = at;     // as many as are needed, or all there are
@@ -421,22 +475,23 @@ compact_kernel(const __grid_constant__ gdn_page_table t, int32_t *const map, con
     __shared__ int s_warp[32];
     __shared__ int s_used;
     launch_dependents();
-    const int P = t.num_pages;
-    const bool vec = ((uintptr_t)t.ref_count & 15) == 0;
-    const int share = ((P + blocks - 1) / blocks + kPer - 1) / kPer * kPer;
+    const int P = t.num_pages, lane = tid & 31;
+    const int share = ((P + blocks - 1) / blocks + 31) / 32 * 32;
     const int p0 = min(rank * share, P), p1 = min(p0 + share, P);
-    const bool once = share <= kThreads * kPer;     // what is counted need not be read again
+    const int per = words_of(p1 - p0), pass = kThreads * per;
+    const bool once = p1 - p0 <= pass;          // what is counted need not be read again
+    const int warp_at = (tid >> 5) * 32 * per;
     // the steps' order: among the blocks, or the threads of the only one
     auto meet = [&]() {
         if (blocks > 1) cluster.sync(); else __syncthreads();
     };
-    uint32_t in = 0, used = 0;
+    Used u;
     int mine = 0, sum;
-    for (int p = p0 + tid * kPer; p < p1; p += kThreads * kPer) {
-        used = used_pages(t.ref_count, p, p1, vec, &in);
-        mine += __popc(used);
+    for (int q = p0; q < p1; q += pass) {
+        u.look(t.ref_count, q + warp_at, p1, per);
+        mine += u.used();
     }
-    const int mine_at = block_scan<int>(mine, s_warp, &sum);
+    const int mine_at = warps_scan(mine, s_warp, &sum);
     int at = 0, U = sum;
     if (blocks > 1) {
         if (tid == 0) s_used = sum;
@@ -450,24 +505,26 @@ compact_kernel(const __grid_constant__ gdn_page_table t, int32_t *const map, con
     }
     // Of the pages in order, `at` are used before p.  A used page of number >= U is the
     // (at - used before U)-th to move, a free one below U the (p - at)-th place.
-    for (int q0 = p0; q0 < p1; q0 += kThreads * kPer) {
-        const int p = q0 + tid * kPer;
+    for (int q0 = p0; q0 < p1; q0 += pass) {
+        const int p = q0 + warp_at;
         int k = at + mine_at;
         if (!once) {
-            used = used_pages(t.ref_count, p, p1, vec, &in);
-            k = at + block_scan<int>(__popc(used), s_warp, &sum);
+            u.look(t.ref_count, p, p1, per);
+            k = at + warps_scan(u.used(), s_warp, &sum);
             at += sum;
         }
+        k = __shfl_sync(0xffffffffu, k, 0);
 #pragma unroll
         for (int e = 0; e < kPer; ++e) {
-            if (!((in >> e) & 1)) continue;
-            const int q = p + e;
-            const bool is = (used >> e) & 1;
-            if (q == U) ws.count[1] = k;
+            if (32 * e >= u.left) break;
+            const int q = p + 32 * e + lane, kk = k + __popc(u.w[e] & ((1u << lane) - 1));
+            k += __popc(u.w[e]);
+            if (!(u.in(e) >> lane & 1)) continue;
+            const bool is = u.w[e] >> lane & 1;
+            if (q == U) ws.count[1] = kk;
             map[q] = is ? q : -1;
-            if (is && q >= U && in_range(k, 1, P, status)) ws.used[k] = q;
-            if (!is && q < U && in_range(q - k, 1, P, status)) ws.open[q - k] = q;
-            k += is;
+            if (is && q >= U && in_range(kk, 1, P, status)) ws.used[kk] = q;
+            if (!is && q < U && in_range(q - kk, 1, P, status)) ws.open[q - kk] = q;
         }
     }
     meet();

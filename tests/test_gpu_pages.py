@@ -187,6 +187,20 @@ def test_many_rows_and_pages(gdn):
     assert s.model.status == 0
 
 
+@pytest.mark.parametrize("n", [700, 2000, 3500])
+def test_rows_listed_twice(gdn, n):
+    """Among hundreds and thousands of listed rows (some of them far past the table), a few twice."""
+    rng = np.random.default_rng(n)
+    s = State(4000, 3, 9000, 4, pools=1, slots=1, seed=n)
+    rows = rng.permutation(4000)[:n].tolist()
+    for i in range(0, n - 50, 97):
+        rows[i + 50] = rows[i]
+    rows[3] = rows[4] = 0x7fffffff
+    rows[8] = -3
+    s.resize(gdn, rows, [int(x) for x in rng.integers(0, 13, n)])
+    assert s.model.status == gdn.GDN_DEV_CONFLICT | gdn.GDN_DEV_BAD_SLOT
+
+
 def test_many_children(gdn):
     s = State(1800, 4, 300, 4, pools=1, slots=1, seed=3)
     s.resize(gdn, [7, 9], [13, 6])
