@@ -23,6 +23,7 @@ constexpr int kThreads = 1024;          // of one
 constexpr int kChunk = 256;             // table entries a warp takes at a time
 constexpr int kPer = 16;                // pages a thread takes at a time at most, 32 apart
 constexpr int kNear = 1024;             // listed rows whose plan is kept in shared memory
+constexpr int kFewEntries = 24 * 1024;  // of the table, that one block changes faster than a cluster
 constexpr int kSlots = 4096;            // of the table that finds rows listed twice
 constexpr int kHashed = 3072;           // listed rows that it is used for
 constexpr int kCopyThreads = 256;
@@ -213,9 +214,9 @@ resize_kernel(const __grid_constant__ gdn_page_table t, const int32_t *row_list,
               const int n, const ResizeWork ws, int32_t *status)
 {
     cg::cluster_group cluster = cg::this_cluster();
-    const int blocks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    int blocks = (int)cluster.num_blocks();
+    const int rank = (int)cluster.block_rank();
     const int tid = threadIdx.x, lane = tid & 31;
-    const int warps = blocks * (kThreads / 32), gw = (tid >> 5) * blocks + rank;    // of the cluster
     __shared__ int s_warp[32];
     __shared__ long long s_wide[32];
     __shared__ int s_most[2];
@@ -305,6 +306,12 @@ resize_kernel(const __grid_constant__ gdn_page_table t, const int32_t *row_list,
     }
     __syncthreads();
     const int most_gone = s_most[0], most_new = s_most[1];
+    // a wide table of which little changes (a step of decoding): the first block does it alone
+    if (blocks > 1 && t.num_pages <= kThreads * kPer && (int64_t)n * (most_gone + most_new) <= kFewEntries) {
+        if (rank > 0) return;
+        blocks = 1;
+    }
+    const int warps = blocks * (kThreads / 32), gw = (tid >> 5) * blocks + rank;    // of those at work
 
     // 2. pages past the new lengths go back; a warp takes kChunk entries of a row at a time
     for (int j00 = 0; j00 < most_gone; j00 += kChunk)
@@ -702,15 +709,15 @@ cudaError_t launch_cluster(void (*kernel)(KA...), int blocks, cudaStream_t strea
     return cudaLaunchKernelEx(&cfg, kernel, KA(args)...);
 }
 
-// One block for tables that it passes over at once and lists that may change some ten thousand
-// entries; else a cluster.  Two calls of 16 to 200 rows on rows of 129 entries: 16, 25 (128 rows:
-// 16512 entries), 55 us on one block, 21, 27, 36 us on a cluster.
+// One block for tables that it passes over at once and lists that may change up to kFewEntries
+// entries; else a cluster.  Two calls of 16, 128, 200, 400 rows on rows of 129 entries: 18, 24, 29,
+// 41 us on one block, 26, 28, 29, 30 us on a cluster.
 bool small_resize(const gdn_page_table &t, int n)
 {
-    return t.num_pages <= kThreads * kPer && (int64_t)n * t.width <= kThreads * 24;
+    return t.num_pages <= kThreads * kPer && (int64_t)n * t.width <= kFewEntries;
 }
-// 3000, 6000, 12000 pages in order: 14, 22, 37 us on one block, 16, 21, 31 us on a cluster.
-bool small_compact(const gdn_page_table &t) { return t.num_pages <= kThreads * 4; }
+// 3000, 6000, 12000 pages in order: 12, 19.5, 31 us on one block, 16, 21, 31 us on a cluster.
+bool small_compact(const gdn_page_table &t) { return t.num_pages <= kThreads * 8; }
 
 uint64_t up16(uint64_t x) { return (x + 15) / 16 * 16; }
 

@@ -187,6 +187,20 @@ def test_many_rows_and_pages(gdn):
     assert s.model.status == 0
 
 
+def test_small_steps_of_a_wide_table(gdn):
+    """Decoding steps: hundreds of rows of a wide table, each longer by a token or two, or cut."""
+    rng = np.random.default_rng(8)
+    s = State(400, 100, 5000, 4, pools=1, slots=1, seed=8)
+    rows = rng.permutation(400).tolist()
+    s.resize(gdn, rows, [int(x) for x in rng.integers(1, 30, 400)])
+    for step in range(6):
+        rows = rng.permutation(400)[:380].tolist()
+        s.resize(gdn, rows, [max(0, s.model.seq[r] + int(rng.integers(-2, 4))) for r in rows])
+        if step == 2:
+            s.fork(gdn, [int(x) for x in range(50)], [int(x) for x in range(350, 400)])
+    assert s.model.status == 0
+
+
 @pytest.mark.parametrize("n", [700, 2000, 3500])
 def test_rows_listed_twice(gdn, n):
     """Among hundreds and thousands of listed rows (some of them far past the table), a few twice."""
