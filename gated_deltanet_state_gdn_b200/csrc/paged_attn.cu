@@ -433,13 +433,13 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                 }
             }
         }
-        if (s_abort) {      // no copy may land after the block is gone: a short wait for each stage
-            const long long start = clock64();
-            for (int k = i > kStages ? i - kStages : 0; k < i; ++k)
-                while (!sm100::mbar_try_wait(full0 + 8 * (k % kStages), (k / kStages) & 1) &&
-                       clock64() - start < (1ll << 26)) {
-                }
-        }
+        // no copy may land after the block is gone, whoever gives up: a wait for the last ones, far
+        // longer than they take and not for good
+        const long long start = clock64();
+        for (int k = i > kStages ? i - kStages : 0; k < i; ++k)
+            while (!sm100::mbar_try_wait(full0 + 8 * (k % kStages), (k / kStages) & 1) &&
+                   clock64() - start < (1ll << 26)) {
+            }
         return;
     }
 
