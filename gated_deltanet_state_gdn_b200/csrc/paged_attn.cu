@@ -31,6 +31,7 @@
 //     and a second kernel joins them in the order of the tokens: no atomics, the same result in
 //     every run.
 #include <cudaTypedefs.h>
+#include <float.h>
 
 #include <algorithm>
 #include <type_traits>
@@ -80,6 +81,10 @@ struct Cfg {
     static constexpr int NX = STEP / 8;              // blocks of 8 columns of scores
     static constexpr int DW = DP / WD;               // dimensions a warp accumulates
     static constexpr int RMAX = 16 * WR;             // rows of a unit
+    // Weights are 2^(x - base) with the base this far below the running maximum: those that meet
+    // the values in fp16 are at most 2^15 (fp16 ends at 65504), so that fp16 holds weights down to
+    // 2^-29 of the largest as normal numbers, not to 2^-14 (bf16 has the range of fp32).
+    static constexpr int UP = KIND == kBF16 ? 0 : 15;
     static constexpr int SMEM = kStages * 2 * kHalfStage + kMergeBytes + kAlign;
     static_assert(WT >= 1 && NS >= 1, "four warps");
 };
@@ -219,13 +224,27 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volati
     return __all_sync(0xffffffffu, came);
 }
 
-template <bool BF16>
-__device__ __forceinline__ uint32_t pack16(float lo, float hi)
+// What the weights of a row with running maximum m are relative to.  Any base does as long as m, l
+// and O of a part go by the same; without a maximum (-inf) it is finite, so that scores of -inf
+// weigh nothing.
+template <class C>
+__device__ __forceinline__ float base_of(float m)
 {
-    if constexpr (BF16)
+    return fmaxf(m, -FLT_MAX) - C::UP;
+}
+
+// two weights for a product in 16 bits (where scores come in steps of 8 or 16 the base may be rounded
+// to 16 below the maximum, and that weight, 2^16, becomes 65504: 2^-11 of it less)
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack_weights(float lo, float hi)
+{
+    if constexpr (BF16) {
         return gdn::pack_bf16x2(lo, hi);
-    else
-        return pack_f16x2(lo, hi);
+    } else {
+        uint32_t d;
+        asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+        return d;
+    }
 }
 
 __device__ __forceinline__ uint32_t pack_out(bool bf16, float lo, float hi)
@@ -674,7 +693,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                 float f[E];
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
-                    f[e] = ex2_approx(m[e] - (mn[e] == -INFINITY ? 0.f : mn[e]));
+                    f[e] = ex2_approx(base_of<C>(m[e]) - base_of<C>(mn[e]));
                     m[e] = mn[e];
                     l[e] *= f[e];
                 }
@@ -685,7 +704,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             }
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                const float mm = m[e] == -INFINITY ? 0.f : m[e];
+                const float mm = base_of<C>(m[e]);
 #pragma unroll
                 for (int n = 0; n < NX; ++n)
 #pragma unroll
@@ -705,9 +724,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                 sm100::fence_proxy_async_smem();
                 __syncwarp();
             }
-            // Times the values: the probabilities rounded to the 16-bit type of the product (off
-            // by 2^-8 of it at most for bf16, 2^-11 for fp16, to nearest, so over many tokens well
-            // below the rounding of the output); l keeps them unrounded.
+            // Times the values: the weights rounded to the 16-bit type of the product (off by 2^-8
+            // of it at most for bf16, 2^-11 for fp16, to nearest, so over many tokens well below
+            // the rounding of the output; in fp16 those below 2^-29 of the row's largest by 2^-40
+            // of that one); l keeps them unrounded.
             auto values = [&](auto clean) {
                 // `clean`: infinities and NaN are taken out before the product, where a row must
                 // not meet the values of a token that another row sees
@@ -731,7 +751,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                 for (int u = 0; u < NX / 2; ++u)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        p[u][k] = pack16<BF16>(x[2 * u + k / 2][2 * (k & 1)], x[2 * u + k / 2][2 * (k & 1) + 1]);
+                        p[u][k] = pack_weights<BF16>(x[2 * u + k / 2][2 * (k & 1)], x[2 * u + k / 2][2 * (k & 1) + 1]);
                 if constexpr (KIND != kE4M3) {
 #pragma unroll
                     for (int u = 0; u < NX / 2; ++u) {
@@ -811,6 +831,7 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             for (int e = 0; e < E; ++e) {
                 l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
                 l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
+                m[e] = base_of<C>(m[e]);        // what l and O are relative to, from here on
             }
             if constexpr (KIND == kE4M3) {
                 const float vsc = kv.v_scale ? __ldg(kv.v_scale + h) : 1.f;

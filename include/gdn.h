@@ -442,7 +442,8 @@ GDN_API gdn_status gdn_kv_append(const void *k, const void *v, int64_t k_token_s
  * `window` only.  Query head h reads head floor(h * H / Hq) of the cache:
  *     x_j = scale * q . k_j,   lse = log sum_j exp(x_j),   out = sum_j exp(x_j - lse) v_j
  * in float32 (scores, maxima, sums and accumulators), with the probabilities rounded to the
- * cache's 16-bit type (fp16 for GDN_E4M3) before they meet the values.  A token that sees
+ * cache's 16-bit type (fp16 for GDN_E4M3) before they meet the values; in fp16 those below 2^-29
+ * of the row's largest are off by up to 2^-40 of the largest instead.  A token that sees
  * nothing (n = 0, or fewer than T positions) gets out = 0 and lse = -inf; a position whose
  * score is -inf has no weight.  Positions that a token does not see never reach its output,
  * whatever they hold (infinities and NaN included).

@@ -6,7 +6,7 @@ import numpy as np
 import pytest
 import torch
 
-from _paged import Case, attend, check_attend, pages_of, wide
+from _paged import HALF_STEP, Case, attend, check_attend, pages_of, wide
 
 pytestmark = pytest.mark.gpu
 
@@ -310,3 +310,50 @@ def test_append_skips_and_tells(gdn):
     if 0 <= int(c.table[s[3], last // 16]) < c.P:
         k0[int(c.table[s[3], last // 16]), last % 16] = new[3, 0]
     assert torch.equal(k, k0)
+
+
+# ---------------------------------------------------------------- weights far below the largest
+@pytest.mark.parametrize("dtype,cache", [(F16, F16), (BF16, E4M3), (BF16, BF16)])
+@pytest.mark.parametrize("nats", [12, 18, 26])
+def test_a_dominant_token_of_no_value(gdn, dtype, cache, nats):
+    """The first token outweighs each other one by e^nats and its value is zero: the output is the
+    others' weighted mean.  In fp16 products a weight of w times the largest is off by half a step
+    of fp16 (2^-11 of it), or by 2^-40 of the largest where w is below 2^-29."""
+    B, n, D = 300, 1024, 64                 # a unit a block: the tokens share a running maximum
+    c = Case(nats, [n] * B, Hq=1, H=1, D=D, dtype=dtype, cache=cache, page=64)
+    c.k = (c.k.float() / 16).to(cache)      # scores of the others: below 1
+    c.v = (c.v.float().abs() * 16 + 100).to(cache)
+    if c.v_scale is not None:
+        c.v_scale = c.v_scale * 2.0 ** (nats - 4)
+    elif dtype == BF16:
+        c.v = (c.v.float() * 2.0 ** nats).to(cache)
+    for b in range(B):
+        q, p = c.q[b, 0, 0].double(), int(c.table[int(c.slots[b]), 0])
+        scale = 1.0 if c.k_scale is None else float(c.k_scale[0])
+        c.k[p, 0, 0] = (q * (nats * math.sqrt(D) / float(q @ q) / scale)).to(cache)
+        c.v[p, 0, 0] = 0
+    want = attend(c)
+    got = c.attend(gdn)
+    if cache != BF16:
+        # the largest weight is one of `total`; what lies below 2^-29 of it adds 2^-40 of it each
+        v = wide(c.v).max() * (1.0 if c.v_scale is None else float(c.v_scale[0]))
+        low = n * 2.0 ** -40 * v / HALF_STEP[F16] / 1.01
+        want = (want[0], want[1], want[2] + low, *want[3:])
+    assert (want[0] > 0).all()
+    check_attend(c, got, want)
+
+
+@pytest.mark.parametrize("dtype,cache", [(F16, F16), (BF16, E4M3), (BF16, BF16)])
+def test_scores_of_any_size(gdn, dtype, cache):
+    """A token alone has weight one whatever its score: up to where scores in fp32 come in steps of
+    2^9 (a weight and the output are rounded once each)."""
+    c = Case(34, [1] * 40, Hq=2, H=2, dtype=dtype, cache=cache, scales=False)
+    rows = [int(c.table[int(s), 0]) for s in c.slots]
+    v = torch.stack([c.v[p, 0] for p in rows]).double()[:, None]
+    for power in range(0, 34):
+        out, lse = c.attend(gdn, scale=2.0 ** power)
+        x = torch.einsum("bthd,bhd->bth", c.q.double(), torch.stack([c.k[p, 0] for p in rows]).double())
+        half = HALF_STEP[BF16 if cache == BF16 else F16] + HALF_STEP[dtype]
+        assert ((out.cpu().double() - v).abs() <= 1.01 * half * v.abs() + 2.0 ** -25).all(), power
+        bound = 2.0 ** power * 68 * 2.0 ** -23 * 64 * 16     # |q| |k| below 4 each
+        assert ((lse.cpu().double() - x * 2.0 ** power).abs() <= bound + 1e-6).all(), power
