@@ -239,22 +239,20 @@ def gdn_paged_attn(q, k_cache, v_cache, block_table, seq_lens, slots=None, *, sc
     cache, heads, cache_dim, code, _ = _cache(k_cache, v_cache, block_table, seq_lens, k_scale, v_scale)
     q, qt, qh = _row_strides("q", q, 0, cache_dim, 2)
     slots = _ints("slots", slots, B, device)
-    flags = 0
-    if (out is None) != (lse is None) and (out is not None or return_lse):
-        # one of the two is the caller's: its padding rows are kept, so the other is cleared here
-        if out is None:
-            out = torch.zeros((B, T, Hq, D), dtype=q.dtype, device=device)
-        else:
-            lse = torch.full((B, T, Hq), -math.inf, device=device) if return_lse else None
-    if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
-        flags = b.GDN_ZERO_PADDING
-    else:
-        _tensor("out", out, q.dtype, (B, T, Hq, D), device)
+    # Padding rows of a given tensor are kept.  Where both are made here the call clears theirs; one
+    # made beside a given one is cleared first.
+    flags = b.GDN_ZERO_PADDING if out is None and lse is None else 0
     if lse is not None:
         _tensor("lse", lse, torch.float32, (B, T, Hq), device)
     elif return_lse:
-        lse = q.new_empty((B, T, Hq), dtype=torch.float32)
+        lse = torch.full((B, T, Hq), -math.inf, device=device) if out is not None else \
+            q.new_empty((B, T, Hq), dtype=torch.float32)
+    if out is not None:
+        _tensor("out", out, q.dtype, (B, T, Hq, D), device)
+    elif flags:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    else:
+        out = torch.zeros((B, T, Hq, D), dtype=q.dtype, device=device)
     L = b.lib()
     nbytes = _attn_workspace(L, device, B, T, Hq, heads, D, code)
     ws = q.new_empty((max(nbytes, 16),), dtype=torch.uint8)

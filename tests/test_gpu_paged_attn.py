@@ -357,3 +357,13 @@ def test_scores_of_any_size(gdn, dtype, cache):
         assert ((out.cpu().double() - v).abs() <= 1.01 * half * v.abs() + 2.0 ** -25).all(), power
         bound = 2.0 ** power * 68 * 2.0 ** -23 * 64 * 16     # |q| |k| below 4 each
         assert ((lse.cpu().double() - x * 2.0 ** power).abs() <= bound + 1e-6).all(), power
+
+
+def test_given_lse_alone_keeps_its_padding_rows(gdn):
+    c = Case(31, [5, 40, 0, 7], pad=(1, 3), T=2)
+    want, wl = c.attend(gdn)
+    lse = torch.full((4, 2, 4), 9.0, device="cuda")
+    out, got = c.attend(gdn, lse=lse, return_lse=False)
+    live = [0, 2]
+    assert got is lse and torch.equal(out, want) and torch.equal(lse[live], wl[live])
+    assert (lse[[1, 3]] == 9).all()
