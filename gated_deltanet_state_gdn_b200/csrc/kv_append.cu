@@ -22,19 +22,21 @@ constexpr int kMaxTokens = 32;    // of a chunk: a lane of the placing warp each
 constexpr int kBlocksSM = 4;
 constexpr int kOffsets = 1024;    // offsets that a block searches in shared memory
 
-// x / scale to nearest, for a quotient within +-1024 (past 448 every quotient is stored as 448, so
-// there the product with the reciprocal will do, infinities included).  With r the reciprocal
-// rounded to nearest, one step of the remainder from x r gives the rounded quotient (Markstein,
-// "Computation of elementary functions on the IBM RISC System/6000 processor", 1990).
+// x / scale to nearest for a scale > 0, for a quotient within +-1024 (past 448 every quotient is
+// stored as 448, so there the product with the reciprocal will do, infinities included).  With r the
+// reciprocal rounded to nearest, one step of the remainder from x r gives the rounded quotient
+// (Markstein, "Computation of elementary functions on the IBM RISC System/6000 processor", 1990).
+// The remainder is taken as q scale - x: where it is zero it is +0, its product with -r is -0, and a
+// quotient of -0 stays one.
 __device__ __forceinline__ float quotient(float x, float scale, float r)
 {
     const float q = x * r;
-    const float y = fmaf(fmaf(-q, scale, x), r, q);
+    const float y = fmaf(fmaf(q, scale, -x), -r, q);
     return fabsf(q) < 1024.f ? y : q;
 }
 
-// eight 16-bit values -> eight e4m3 numbers of x / scale
-__device__ __forceinline__ uint2 quantise(const uint4 &w, bool bf16, float scale, float r, bool plain)
+// eight 16-bit values -> eight e4m3 numbers of x / scale, the sign of a negative scale in `flip`
+__device__ __forceinline__ uint2 quantise(const uint4 &w, bool bf16, float scale, float r, bool plain, uint32_t flip)
 {
     const uint32_t in[4] = {w.x, w.y, w.z, w.w};
     uint32_t out[2] = {0u, 0u};
@@ -54,7 +56,7 @@ __device__ __forceinline__ uint2 quantise(const uint4 &w, bool bf16, float scale
         // to the largest number; a NaN stays one)
         out[k / 2] |= (uint32_t)__nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3) << (16 * (k & 1));
     }
-    return make_uint2(out[0], out[1]);
+    return make_uint2(out[0] ^ flip, out[1] ^ flip);
 }
 
 // where token n goes: element offset of its head 0 in the cache, or -1; `offsets` are the row
@@ -156,13 +158,16 @@ kv_append_kernel(const __grid_constant__ GdnAppendArgs a, const int tokens, cons
             const int64_t off = h * kv.head_stride + d;
             unsigned char *const y = static_cast<unsigned char *>(v ? kv.v : kv.k) + off * (E4M3 ? 1 : 2);
             float scale = 1.f, inv = 1.f;
+            uint32_t flip = 0u;
             if (E4M3 && mine) {
                 const float *const sc = v ? kv.v_scale : kv.k_scale;
                 if (sc) scale = __ldg(sc + h);
+                if (signbit(scale)) flip = 0x80808080u;
+                scale = fabsf(scale);
                 inv = __frcp_rn(scale);
             }
             // (a scale whose reciprocal is no normal number is divided by)
-            const bool plain = fabsf(scale) > 0x1p-120f && fabsf(scale) < 0x1p120f;
+            const bool plain = scale > 0x1p-120f && scale < 0x1p120f;
 #pragma unroll 1
             for (int i = t0; i - t0 < here; i += side * kHold) {
                 uint4 w[kHold];
@@ -178,7 +183,7 @@ kv_append_kernel(const __grid_constant__ GdnAppendArgs a, const int tokens, cons
                     const int64_t at = mine && t < here ? s_at[buf][t] : -1;
                     if (at < 0 || !in_range(at + off, 8, cache_n, a.dev_status)) continue;
                     if constexpr (E4M3)
-                        *reinterpret_cast<uint2 *>(y + at) = quantise(w[k], a.bf16 != 0, scale, inv, plain);
+                        *reinterpret_cast<uint2 *>(y + at) = quantise(w[k], a.bf16 != 0, scale, inv, plain, flip);
                     else
                         *reinterpret_cast<uint4 *>(y + 2 * at) = w[k];
                 }

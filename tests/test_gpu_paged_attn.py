@@ -367,3 +367,32 @@ def test_given_lse_alone_keeps_its_padding_rows(gdn):
     live = [0, 2]
     assert got is lse and torch.equal(out, want) and torch.equal(lse[live], wl[live])
     assert (lse[[1, 3]] == 9).all()
+
+
+def bytes_of(x, scale):
+    """The e4m3 bytes of x / scale (the quotient in float32), the sign of a zero among them."""
+    with np.errstate(divide="ignore", over="ignore", under="ignore"):
+        y = np.float32(x) / np.float32(scale)
+    a = np.abs(e4m3(y.astype(np.float64)))
+    ex = np.floor(np.log2(np.maximum(a, 2.0 ** -6)))
+    code = np.where(a < 2.0 ** -6, a * 2 ** 9, (ex + 7) * 8 + (a / 2.0 ** ex - 1) * 8)
+    return (code.astype(np.int64) + 128 * np.signbit(y)).astype(np.uint8)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("scale", [None, 1.0, 0.7, -0.7, 3e-3, -250.0, 1e-38, -1e-38, 1e37])
+def test_append_rounds_to_the_same_bytes(gdn, dtype, scale):
+    """Every byte, zeros of both signs and numbers that become zero among them."""
+    g = torch.Generator().manual_seed(3)
+    n, H, D, page = 40, 2, 64, 16
+    x = torch.randn(n, H, D, generator=g) * 2.0 ** torch.randint(-16, 9, (n, H, D), generator=g)
+    x = (x * abs(scale or 1.0)).to(dtype)
+    x[0, :, :8] = torch.tensor([-0.0, 0.0, -1e-7, 1e-7, -2.0 ** -24, 2.0 ** -24, -3.0, 3.0]).to(dtype)
+    k, v = (torch.zeros(3, page, H, D, dtype=E4M3, device="cuda") for _ in range(2))
+    table = torch.tensor([[1, 0, 2]], dtype=torch.int32, device="cuda")
+    sc = None if scale is None else torch.full((H,), scale, device="cuda")
+    gdn.gdn_kv_append(x.cuda(), (-x).cuda(), k, v, table, torch.tensor([n], dtype=torch.int32, device="cuda"),
+                      torch.tensor([0], dtype=torch.int32, device="cuda"), k_scale=sc, v_scale=sc)
+    for got, y in ((k, x), (v, -x)):
+        got = got.view(torch.uint8)[[1, 0, 2]].reshape(-1, H, D)[:n].cpu().numpy()
+        np.testing.assert_array_equal(got, bytes_of(wide(y), scale or 1.0))
