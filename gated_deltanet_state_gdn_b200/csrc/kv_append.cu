@@ -199,6 +199,10 @@ cudaError_t launch_kv_append(const GdnAppendArgs &a, cudaStream_t stream)
     using namespace gdn_append;
     // equal chunks of at most kMaxTokens, in as few rounds of the resident blocks as that takes
     const int64_t resident = (int64_t)kBlocksSM * gdn_cache::sm_count();
+    if (resident == 0) {        // no device, or one that does not answer
+        const cudaError_t e = cudaGetLastError();
+        return e == cudaSuccess ? cudaErrorNoDevice : e;
+    }
     const int64_t rounds = (a.N + resident * kMaxTokens - 1) / (resident * kMaxTokens);
     const int64_t tokens = (a.N + resident * rounds - 1) / (resident * rounds);
     const int64_t chunks = (a.N + tokens - 1) / tokens;

@@ -3,6 +3,7 @@ addresses are never dereferenced), the binding's own checks, and the models that
 compare with."""
 import ctypes
 import math
+import os
 
 import numpy as np
 import pytest
@@ -78,6 +79,31 @@ def test_append_refusals(g):
     assert append(g, N=0) == g.GDN_OK
     # one head, one token a page: their strides do not matter
     assert append(g, cache(heads=1, head_stride=3), kh=5, vh=7, N=0) == g.GDN_OK
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the addresses are made up: no call may be launched")
+def test_calls_without_a_device_return(g):
+    """Valid calls where there is no GPU return an error, in a process of their own (a call that
+    ends the process would end these tests)."""
+    import subprocess
+    import sys
+    code = """if 1:
+        import sys
+        sys.path[:0] = ["tests", "."]
+        import gated_deltanet_state_gdn_b200 as g
+        import test_paged_host as t
+        assert t.append(g) == g.GDN_ERR_CUDA
+        assert t.append(g, t.cache(dtype=3, page_stride=32 * 64)) == g.GDN_ERR_CUDA
+        assert t.attn(g) == g.GDN_ERR_CUDA
+        L, P = g.lib(), t.P
+        assert L.gdn_page_resize(bytes(t.table()), P(5), P(6), 3, None, 0, P(7), 1 << 20, None, None) == g.GDN_ERR_CUDA
+        assert L.gdn_page_fork(bytes(t.table()), P(5), P(6), 3, None, 0, None, None) == g.GDN_ERR_CUDA
+        assert L.gdn_page_compact(bytes(t.table()), P(5), None, 0, P(7), 1 << 20, None, None) == g.GDN_ERR_CUDA
+        print("returned")
+    """
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "returned" in r.stdout, r.stdout + r.stderr
 
 
 def attn(g, c=None, **kw):
