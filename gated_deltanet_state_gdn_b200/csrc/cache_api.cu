@@ -45,6 +45,35 @@ bool apart(const gdn_paged_cache &c)
            (c.num_pages == 1 || c.page_stride >= (H - 1) * hs + (S - 1) * ts + D);
 }
 
+// Whether two rows of bytes `delta` apart meet when either may be moved by whole numbers of steps: by
+// less than dim[i].n of dim[i].step each, a step at least what the dimensions after it span.  The
+// first row is of `a` bytes, the second of `b`.
+struct Steps {
+    int64_t n, step;
+};
+bool rows_meet(int64_t delta, int64_t a, int64_t b, const Steps *dim, int dims)
+{
+    if (dims == 0) return delta < a && -delta < b;
+    // (what is left after the right number of steps is less than one)
+    const int64_t near = dim->n > 1 ? delta / dim->step : 0;
+    for (int64_t k = near - 1; k <= near + 1; ++k)
+        if (-dim->n < k && k < dim->n &&
+            rows_meet(delta - (dim->n > 1 ? k * dim->step : 0), a, b, dim + 1, dims - 1))
+            return true;
+    return false;
+}
+
+// a vector of k and one of v share an element; the vectors of either are apart
+bool keys_meet_values(const gdn_paged_cache &c)
+{
+    const int64_t es = elem_size(c.dtype), row = c.head_dim * es;
+    const Steps page = {c.num_pages, c.page_stride * es}, token = {c.page_size, c.token_stride * es},
+                head = {c.heads, c.head_stride * es};
+    const bool heads_in = c.heads == 1 || (c.page_size > 1 && c.head_stride < c.token_stride);
+    const Steps dim[3] = {page, heads_in ? token : head, heads_in ? head : token};
+    return rows_meet((int64_t)((uintptr_t)c.v - (uintptr_t)c.k), row, row, dim, 3);
+}
+
 gdn_status check_cache(const gdn_paged_cache *c)
 {
     if (!c) return GDN_ERR_NULL;
@@ -133,6 +162,7 @@ gdn_status gdn_kv_append(const void *k, const void *v, int64_t k_token_stride,
     if (st != GDN_OK) return st;
     if (cache->dtype != GDN_E4M3 && cache->dtype != (int32_t)dtype) return GDN_ERR_DTYPE;
     if (!apart(*cache)) return GDN_ERR_SHAPE;
+    if (keys_meet_values(*cache)) return GDN_ERR_ALIAS;
     if (B < 0 || N < 0 || k_token_stride < 0 || k_head_stride < 0 || v_token_stride < 0 ||
         v_head_stride < 0)
         return GDN_ERR_SHAPE;
@@ -158,7 +188,6 @@ gdn_status gdn_kv_append(const void *k, const void *v, int64_t k_token_stride,
             overlaps(c, cb, cache->k_scale, (size_t)cache->heads * 4) ||
             overlaps(c, cb, cache->v_scale, (size_t)cache->heads * 4))
             return GDN_ERR_ALIAS;
-    if (cache->k == cache->v) return GDN_ERR_ALIAS;
 
     GdnAppendArgs a;
     a.k = k; a.v = v;

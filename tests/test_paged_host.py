@@ -106,6 +106,46 @@ def test_calls_without_a_device_return(g):
     assert r.returncode == 0 and "returned" in r.stdout, r.stdout + r.stderr
 
 
+def vectors(base, c):
+    """First bytes of all vectors of a cache, [pages, tokens, heads]."""
+    es = 1 if c.dtype == 3 else 2
+    i, j, h = (np.arange(n) for n in (c.num_pages, c.page_size, c.heads))
+    return base + es * (i[:, None, None] * c.page_stride + j[:, None] * c.token_stride + h * c.head_stride)
+
+
+@pytest.mark.parametrize("dtype", [1, 3])
+@pytest.mark.parametrize("pages,page,heads,D,order,gaps", [
+    (5, 4, 3, 16, "tokens", (0, 0, 0)), (5, 4, 3, 16, "heads", (0, 0, 0)), (4, 3, 2, 16, "tokens", (16, 0, 0)),
+    (4, 3, 2, 32, "tokens", (0, 96, 0)), (4, 3, 2, 16, "heads", (32, 16, 128)), (3, 1, 4, 16, "tokens", (16, 0, 0)),
+    (3, 5, 1, 16, "heads", (0, 16, 32)), (1, 1, 1, 16, "tokens", (0, 0, 0))])
+def test_keys_over_values(g, dtype, pages, page, heads, D, order, gaps):
+    """Caches whose keys and values share bytes are refused for writing, wherever they start; values
+    in the gaps between keys are not."""
+    inner = D + gaps[0]
+    if order == "tokens":
+        hs, ts = inner, heads * inner + gaps[1]
+        ps = page * ts + gaps[2]
+    else:
+        ts, hs = inner, page * inner + gaps[1]
+        ps = heads * hs + gaps[2]
+    es = 1 if dtype == 3 else 2
+    a = dict(dtype=dtype, num_pages=pages, page_size=page, heads=heads, head_dim=D, head_stride=hs, token_stride=ts,
+             page_stride=ps)
+    k = vectors(P(1), cache(**a)).reshape(-1)
+    end = (pages * ps + 4 * D) * es
+    got = {}
+    for off in range(-end // 16 * 16, end, 16):
+        status = append(g, cache(v=P(1, off), **a), kt=heads * D, kh=D, vt=heads * D, vh=D, dtype=1, N=0)
+        v = vectors(P(1, off), cache(**a)).reshape(-1)
+        at = np.searchsorted(v, k)              # a key's vector meets the values' next or last one
+        gap = np.minimum(np.abs(v[np.minimum(at, len(v) - 1)] - k), np.abs(v[np.maximum(at - 1, 0)] - k)) \
+            if (np.diff(v) > 0).all() else np.abs(v[:, None] - k).min(0)
+        want = g.GDN_ERR_ALIAS if (gap < D * es).any() else g.GDN_OK
+        assert status == want, off
+        got[status] = got.get(status, 0) + 1
+    assert len(got) == 2
+
+
 def attn(g, c=None, **kw):
     a = dict(q=P(5), qt=256, qh=64, slots=P(7), B=3, T=2, Hq=4, dtype=1, scale=0.1, window=0, out=P(8), lse=P(9),
              flags=0, ws=P(10), nbytes=1 << 30)
