@@ -4,6 +4,8 @@
 // and pointer values the caller passes.
 #include <string.h>
 
+#include <algorithm>
+
 #include "cache.cuh"
 #include "host_checks.cuh"
 
@@ -121,8 +123,66 @@ bool meets_table(const gdn_page_table &t, const void *p, size_t bytes)
            overlaps(p, bytes, t.seq_lens, (size_t)t.rows * 4);
 }
 
-// Pools of `rows` rows.  Their spans may interleave (keys and values of one tensor), so only a
-// pool listed twice, which two blocks would copy at the same time, is looked for.
+int64_t pool_span(const gdn_pool &p, int32_t rows) { return (int64_t)(rows - 1) * p.row_stride + p.row_bytes; }
+
+// a row of p and one of q share a byte
+bool pools_meet(const gdn_pool &p, const gdn_pool &q, int32_t rows)
+{
+    if (!overlaps(p.data, (size_t)pool_span(p, rows), q.data, (size_t)pool_span(q, rows))) return false;
+    const int64_t delta = (int64_t)((uintptr_t)q.data - (uintptr_t)p.data);
+    if (rows == 1 || p.row_stride == q.row_stride) {
+        const Steps dim = {rows, p.row_stride};
+        return rows_meet(delta, p.row_bytes, q.row_bytes, &dim, 1);
+    }
+    // rows of two spacings in one place: row by row, against the first of q's that ends past it
+    for (int64_t i = 0; i < rows; ++i) {
+        const int64_t at = i * p.row_stride - delta;        // of p's row, from q's first
+        const int64_t k = at < q.row_bytes ? 0 : (at - q.row_bytes) / q.row_stride + 1;
+        if (k < rows && k * q.row_stride < at + p.row_bytes && k * q.row_stride + q.row_bytes > at) return true;
+    }
+    return false;
+}
+
+// Whether two of the pools share bytes, which two blocks would copy at the same time.  Spans may
+// interleave: keys and values of one tensor, its layers.  Up to kSorted pools are gone through in
+// the order of their addresses: a pool past all before it, or beside the last one in rows of the
+// same spacing, need not be compared with each.
+bool any_pools_meet(const gdn_pool *pools, int32_t n, int32_t rows)
+{
+    constexpr int kSorted = 512;
+    int order[kSorted];
+    const bool sorted = n <= kSorted;
+    if (sorted) {
+        for (int i = 0; i < n; ++i) order[i] = i;
+        std::sort(order, order + n,
+                  [&](int i, int j) { return (uintptr_t)pools[i].data < (uintptr_t)pools[j].data; });
+    }
+    auto at = [&](int k) -> const gdn_pool & { return pools[sorted ? order[k] : k]; };
+    auto end = [](const gdn_pool &p, int64_t bytes) { return (uintptr_t)p.data + (uintptr_t)bytes; };
+    int first = 0;              // those from here on reach past one another's beginnings
+    uintptr_t reach = 0;
+    bool beside = true;         // all of them lie side by side, between two rows of the first
+    for (int k = 0; k < n; ++k) {
+        const gdn_pool &q = at(k);
+        const uintptr_t q_end = end(q, pool_span(q, rows));
+        if (sorted && (uintptr_t)q.data >= reach) {
+            first = k;
+            reach = q_end;
+            beside = true;
+            continue;
+        }
+        const gdn_pool &f = at(first);
+        beside = beside && sorted && q.row_stride == f.row_stride &&
+                 (uintptr_t)q.data >= end(at(k - 1), at(k - 1).row_bytes) &&
+                 end(q, q.row_bytes) <= end(f, f.row_stride);
+        for (int j = first; j < k && !beside; ++j)
+            if (pools_meet(at(j), q, rows)) return true;
+        reach = std::max(reach, q_end);
+    }
+    return false;
+}
+
+// Pools of `rows` rows.
 gdn_status check_pools(const gdn_page_table &t, const gdn_pool *pools, int32_t n, int32_t rows)
 {
     if (n < 0) return GDN_ERR_SHAPE;
@@ -132,18 +192,15 @@ gdn_status check_pools(const gdn_page_table &t, const gdn_pool *pools, int32_t n
         if (p.row_bytes < 1 || (rows > 1 && p.row_stride < p.row_bytes)) return GDN_ERR_SHAPE;
         if (p.row_bytes >= (int64_t)1 << 36) return GDN_ERR_UNSUPPORTED;
         if (!p.data) return GDN_ERR_NULL;
-        for (int j = 0; j < i; ++j)
-            if (pools[j].data == p.data) return GDN_ERR_ALIAS;
-        if (meets_table(t, p.data, (size_t)(rows - 1) * p.row_stride + p.row_bytes)) return GDN_ERR_ALIAS;
+        if (meets_table(t, p.data, (size_t)pool_span(p, rows))) return GDN_ERR_ALIAS;
     }
-    return GDN_OK;
+    return any_pools_meet(pools, n, rows) ? GDN_ERR_ALIAS : GDN_OK;
 }
 
 bool meets_pools(const gdn_pool *pools, int32_t n, int32_t rows, const void *p, size_t bytes)
 {
     for (int i = 0; i < n; ++i)
-        if (overlaps(p, bytes, pools[i].data, (size_t)(rows - 1) * pools[i].row_stride + pools[i].row_bytes))
-            return true;
+        if (overlaps(p, bytes, pools[i].data, (size_t)pool_span(pools[i], rows))) return true;
     return false;
 }
 

@@ -490,7 +490,8 @@ typedef struct {
     int32_t num_pages, page_size;
 } gdn_page_table;
 
-/* An array of rows in device memory: row i is the row_bytes bytes at data + i * row_stride. */
+/* An array of rows in device memory: row i is the row_bytes bytes at data + i * row_stride.  The
+ * pools of a call share no bytes (GDN_ERR_ALIAS); rows of one may lie in the gaps of another. */
 typedef struct {
     void *data;
     int64_t row_stride, row_bytes;   /* bytes; row_stride >= row_bytes */

@@ -237,6 +237,44 @@ def test_page_refusals(g):
     assert L.gdn_page_workspace_size(20, 3) > 0 and L.gdn_page_workspace_size(20, 0) > 0
 
 
+def meet(a, b, rows):
+    """Whether a row of one pool shares a byte with a row of another (addresses, strides, lengths)."""
+    x, y = ({(p, p + n) for p in range(at, at + (rows - 1) * s + 1, max(s, 1))} for at, s, n in (a, b))
+    return any(p < e2 and p2 < e for p, e in x for p2, e2 in y)
+
+
+def test_pools_over_one_another(g):
+    """Pools that share bytes are refused, wherever they start; pools in each other's gaps are not.
+    (No row is listed: nothing is launched.)"""
+    L = g.lib()
+    rng = np.random.default_rng(1)
+
+    def fork(rows, some):
+        arr, k = pools(*some)
+        t = table(rows=rows)
+        return L.gdn_page_fork(ctypes.byref(t), P(5), P(6), 0, arr, k, None, None)
+
+    seen = set()
+    for _ in range(3000):
+        rows, n = int(rng.integers(1, 6)), int(rng.integers(2, 6))
+        stride = int(rng.integers(1, 40))
+        some = []
+        for _ in range(n):
+            s = stride if rng.random() < 0.8 else int(rng.integers(1, 90))
+            some.append((P(8, int(rng.integers(0, 120))), s, int(rng.integers(1, min(s, 9) + 1))))
+        want = any(meet(some[i], some[j], rows) for i in range(n) for j in range(i))
+        assert fork(rows, some) == (g.GDN_ERR_ALIAS if want else g.GDN_OK), (rows, some)
+        seen.add((want, len({s for _, s, _ in some}) > 1))
+    assert len(seen) == 4
+    # layers of one tensor, in any order and more than are gone through in order; then one too many
+    for n in (2, 96, 512, 700):
+        some = [(P(8, 64 * int(i)), 64 * n, 64) for i in rng.permutation(n)]
+        assert fork(4, some) == g.GDN_OK
+        assert fork(4, some + [(P(8, 64 * (n + 3) + 8), 64 * n, 8)]) == g.GDN_ERR_ALIAS
+    apart_ = [(P(8, 1000 * int(i)), 64, 64) for i in rng.permutation(300)]
+    assert fork(4, apart_) == g.GDN_OK and fork(4, apart_ + [(P(8, 255), 64, 1)]) == g.GDN_ERR_ALIAS
+
+
 def test_binding_takes_gpu_tensors_only(g):
     x = torch.zeros(1, 1, 2, 64, dtype=torch.bfloat16)
     t = torch.zeros(1, 1, dtype=torch.int32)
