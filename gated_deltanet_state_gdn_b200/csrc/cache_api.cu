@@ -84,6 +84,10 @@ gdn_status check_cache(const gdn_paged_cache *c)
         c->head_dim < 1 || c->page_stride < 0 || c->token_stride < 0 || c->head_stride < 0 ||
         (c->rows > 1 && c->table_stride < c->width))
         return GDN_ERR_SHAPE;
+    // (an expanded view: a box of a tensor map has no steps of zero)
+    if ((c->num_pages > 1 && c->page_stride == 0) || (c->page_size > 1 && c->token_stride == 0) ||
+        (c->heads > 1 && c->head_stride == 0))
+        return GDN_ERR_SHAPE;
     const int es = elem_size(c->dtype);
     if (c->head_dim > 256 || c->head_dim * es % 16 != 0) return GDN_ERR_UNSUPPORTED;
     if ((int64_t)c->width * c->page_size > kMostPositions) return GDN_ERR_UNSUPPORTED;

@@ -389,8 +389,8 @@ GDN_API gdn_status gdn_conv1d(const void *x, const void *weight, void *conv_stat
 typedef struct {
     void *k, *v;             /* device: page p, token o, head h, dimension i at
                                 p*page_stride + o*token_stride + h*head_stride + i, the same
-                                strides for both (in elements, multiples of 16 bytes; that of a
-                                dimension of one does not matter) */
+                                strides for both (in elements, multiples of 16 bytes above
+                                zero; that of a dimension of one does not matter) */
     int64_t page_stride, token_stride, head_stride;
     const float *k_scale, *v_scale;  /* [heads] float32 or NULL (ones): GDN_E4M3 only, what a
                                         stored number is multiplied by to give its value */

@@ -180,6 +180,16 @@ def test_attn_refusals(g):
     assert size(0, 1, 4, 2, 64, 1) == 0 and size(1, 17, 4, 2, 64, 1) == 0 and size(1, 1, 5, 2, 64, 1) == 0
 
 
+def test_expanded_caches_are_refused(g):
+    """A stride of zero, of a dimension of more than one (nothing is launched: B or N is zero)."""
+    for f, kw in ((attn, dict(B=0)), (append, dict(N=0))):
+        for n in ("page_stride", "token_stride", "head_stride"):
+            assert f(g, cache(**{n: 0}), **kw) == g.GDN_ERR_SHAPE
+        assert f(g, cache(heads=1, head_stride=0), **kw) == g.GDN_OK
+        assert f(g, cache(page_size=1, token_stride=0, page_stride=128), **kw) == g.GDN_OK
+        assert f(g, cache(num_pages=1, page_stride=0), **kw) == g.GDN_OK
+
+
 def table(**kw):
     from gated_deltanet_state_gdn_b200._paged import _Table
     a = dict(block_table=P(1), ref_count=P(2), seq_lens=P(3), table_stride=8, rows=4, width=8, num_pages=20,
