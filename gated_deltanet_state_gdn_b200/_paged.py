@@ -85,6 +85,15 @@ def _here(t):
     return 0 if t is None else t.data_ptr()
 
 
+def _status(t, device):
+    """The status word, which the kernels write to: its address."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.device != device or t.dtype != _I32 or t.numel() < 1:
+        raise TypeError(f"dev_status must be an int32 tensor on {device}")
+    return t.data_ptr()
+
+
 @functools.lru_cache(maxsize=256)
 def _attn_workspace(lib, device, *sizes):
     """gdn_paged_attn_workspace_size: it depends on the device and these sizes alone."""
@@ -210,7 +219,7 @@ def gdn_kv_append(k, v, k_cache, v_cache, block_table, seq_lens, slots=None, row
     row_offsets = _ints("row_offsets", row_offsets, B + 1, device)
     _raise(b.lib().gdn_kv_append(_at(k), _at(v), kt, kh, vt, vh, cache,
                                  _at(slots), _at(row_offsets), B, N, dt,
-                                 _at(dev_status), _stream(device)), "gdn_kv_append")
+                                 _status(dev_status, device), _stream(device)), "gdn_kv_append")
     return k_cache, v_cache
 
 
@@ -259,7 +268,7 @@ def gdn_paged_attn(q, k_cache, v_cache, block_table, seq_lens, slots=None, *, sc
     _raise(L.gdn_paged_attn(_at(q), qt, qh, cache, _at(slots), B, T, Hq, dt,
                             1.0 / math.sqrt(D) if scale is None else float(scale), int(window),
                             _at(out), _at(lse), flags, _at(ws), nbytes,
-                            _at(dev_status), _stream(device)), "gdn_paged_attn")
+                            _status(dev_status, device), _stream(device)), "gdn_paged_attn")
     return out if lse is None else (out, lse)
 
 
@@ -322,7 +331,7 @@ def gdn_page_resize(block_table, ref_count, seq_lens, row_list, new_lens, page_s
     nbytes = L.gdn_page_workspace_size(num_pages, max(n, 1))
     ws = block_table.new_empty((nbytes,), dtype=torch.uint8)
     _raise(L.gdn_page_resize(t, _at(row_list), _at(new_lens), n, arr, count,
-                             _at(ws), nbytes, _at(dev_status), _stream(device)),
+                             _at(ws), nbytes, _status(dev_status, device), _stream(device)),
            "gdn_page_resize")
     return block_table, ref_count, seq_lens
 
@@ -344,7 +353,7 @@ def gdn_page_fork(block_table, ref_count, seq_lens, parents, children, page_size
     children = _ints("children", children, n, device)
     arr, count = _pools(pools, rows, device)
     _raise(b.lib().gdn_page_fork(t, _at(parents), _at(children), n, arr,
-                                 count, _at(dev_status), _stream(device)), "gdn_page_fork")
+                                 count, _status(dev_status, device), _stream(device)), "gdn_page_fork")
     return block_table, ref_count, seq_lens
 
 
@@ -367,5 +376,5 @@ def gdn_page_compact(block_table, ref_count, seq_lens, page_size: int, pools=(),
     nbytes = L.gdn_page_workspace_size(num_pages, 0)
     ws = block_table.new_empty((nbytes,), dtype=torch.uint8)
     _raise(L.gdn_page_compact(t, _at(page_map), arr, count, _at(ws), nbytes,
-                              _at(dev_status), _stream(device)), "gdn_page_compact")
+                              _status(dev_status, device), _stream(device)), "gdn_page_compact")
     return page_map

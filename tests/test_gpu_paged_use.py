@@ -249,6 +249,22 @@ def test_wrong_devices_are_refused(gdn):
         gdn.gdn_paged_attn(*args, lse=torch.zeros(1, 1, 3, device="cuda"))
 
 
+def test_status_on_the_host_is_refused(gdn):
+    s = Server(21)
+    calls = [lambda st: gdn.gdn_kv_append(s.kn, s.vn, s.k, s.v, s.table, s.seq, s.slots, dev_status=st),
+             lambda st: gdn.gdn_paged_attn(s.q, s.k, s.v, s.table, s.seq, s.slots, dev_status=st),
+             lambda st: gdn.gdn_page_resize(s.table, s.ref, s.seq, s.rows, s.lens, s.page, dev_status=st),
+             lambda st: gdn.gdn_page_fork(s.table, s.ref, s.seq, ints([0]), ints([1]), s.page, dev_status=st),
+             lambda st: gdn.gdn_page_compact(s.table, s.ref, s.seq, s.page, dev_status=st)]
+    before = s.everything()
+    for call in calls:
+        for bad in (torch.zeros(1, dtype=torch.int32), torch.zeros(1, device="cuda"),
+                    torch.zeros(1, dtype=torch.int64, device="cuda")):
+            with pytest.raises(TypeError, match="dev_status"):
+                call(bad)
+    assert same(before, s.everything())
+
+
 def both(gdn, fn):
     """fn(status) through the product library, then through the checked build."""
     product = gdn._binding.LIB_PATH

@@ -308,6 +308,19 @@ def test_packed_structures():
         assert bytes(cls(*values)) == packed.pack(*values)
 
 
+def test_status_word():
+    """What the kernels write their status to: an int32 tensor of the call's device."""
+    from gated_deltanet_state_gdn_b200._paged import _status
+    dev = torch.device("cpu")
+    t = torch.zeros(4, dtype=torch.int32)
+    assert _status(None, dev) is None and _status(t, dev) == t.data_ptr() and _status(t[2], dev) == t[2].data_ptr()
+    for bad in (t.long(), t.float(), t[:0], [0], 0):
+        with pytest.raises(TypeError, match="dev_status"):
+            _status(bad, dev)
+    with pytest.raises(TypeError, match="dev_status"):
+        _status(t, torch.device("cuda", 0))
+
+
 def test_row_strides():
     """What the binding takes for evenly spaced tokens, and what it copies."""
     from gated_deltanet_state_gdn_b200._paged import _row_strides
