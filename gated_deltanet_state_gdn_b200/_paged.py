@@ -18,6 +18,7 @@ from . import _binding as b
 _DTYPES = {torch.bfloat16: b.GDN_BF16, torch.float16: b.GDN_F16}
 _CACHE_DTYPES = {**_DTYPES, torch.float8_e4m3fn: b.GDN_E4M3}
 _I32 = torch.int32
+_NO_WINDOW = 1 << 30          # positions a row can hold at most: as far as a window can reach
 
 
 class _Cache(ctypes.Structure):
@@ -266,7 +267,7 @@ def gdn_paged_attn(q, k_cache, v_cache, block_table, seq_lens, slots=None, *, sc
     nbytes = _attn_workspace(L, device, B, T, Hq, heads, D, code)
     ws = q.new_empty((max(nbytes, 16),), dtype=torch.uint8)
     _raise(L.gdn_paged_attn(_at(q), qt, qh, cache, _at(slots), B, T, Hq, dt,
-                            1.0 / math.sqrt(D) if scale is None else float(scale), int(window),
+                            1.0 / math.sqrt(D) if scale is None else float(scale), min(int(window), _NO_WINDOW),
                             _at(out), _at(lse), flags, _at(ws), nbytes,
                             _status(dev_status, device), _stream(device)), "gdn_paged_attn")
     return out if lse is None else (out, lse)

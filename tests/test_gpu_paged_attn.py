@@ -396,3 +396,10 @@ def test_append_rounds_to_the_same_bytes(gdn, dtype, scale):
     for got, y in ((k, x), (v, -x)):
         got = got.view(torch.uint8)[[1, 0, 2]].reshape(-1, H, D)[:n].cpu().numpy()
         np.testing.assert_array_equal(got, bytes_of(wide(y), scale or 1.0))
+
+
+def test_windows_past_32_bits(gdn):
+    c = Case(32, [70, 40, 300], T=2)
+    want = c.attend(gdn)
+    for window in (1 << 30, (1 << 31) - 1, 1 << 31, (1 << 32) + 5, 1 << 70):
+        assert all(torch.equal(a, b) for a, b in zip(c.attend(gdn, window=window), want)), window
