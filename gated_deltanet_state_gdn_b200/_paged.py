@@ -191,10 +191,10 @@ def gdn_kv_append(k, v, k_cache, v_cache, block_table, seq_lens, slots=None, row
                   k_scale=None, v_scale=None, dev_status=None):
     """Write new tokens' keys and values to the pages of their positions.
 
-    k, v: [N, heads, D] or [B, T, heads, D], bf16 or fp16 (views of a packed projection are read
-    where they lie); k_cache, v_cache: [num_pages, page_size, heads, D] of the same type or
-    float8_e4m3fn (any strides with D dense, the same for both), written in place; block_table:
-    [rows, width] int32; seq_lens: [rows] int32, counting the new tokens already; slots: [B]
+    k, v: [N, heads, D] ([1, N, heads, D] likewise) or [B, T, heads, D], bf16 or fp16 (views of a
+    packed projection are read where they lie); k_cache, v_cache: [num_pages, page_size, heads, D]
+    of the same type or float8_e4m3fn (any strides with D dense, the same for both), written in
+    place; block_table: [rows, width] int32; seq_lens: [rows] int32, counting the new tokens already; slots: [B]
     int32 rows of the table (negative: padding) or None (request b is row b); row_offsets: [B+1]
     int32, or None for equally many tokens a request; k_scale, v_scale: [heads] fp32 or None,
     for an 8-bit cache.  Returns (k_cache, v_cache).
@@ -216,6 +216,8 @@ def gdn_kv_append(k, v, k_cache, v_cache, block_table, seq_lens, slots=None, row
         B = row_offsets.shape[0] - 1
     else:
         B = k.shape[0] if k.dim() == 4 else rows
+    if k.dim() == 4 and row_offsets is None and k.shape[0] not in (1, B):
+        raise ValueError(f"k has {k.shape[0]} requests, slots {B}")
     slots = _ints("slots", slots, B, device)
     row_offsets = _ints("row_offsets", row_offsets, B + 1, device)
     _raise(b.lib().gdn_kv_append(_at(k), _at(v), kt, kh, vt, vh, cache,

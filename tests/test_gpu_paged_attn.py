@@ -403,3 +403,24 @@ def test_windows_past_32_bits(gdn):
     want = c.attend(gdn)
     for window in (1 << 30, (1 << 31) - 1, 1 << 31, (1 << 32) + 5, 1 << 70):
         assert all(torch.equal(a, b) for a, b in zip(c.attend(gdn, window=window), want)), window
+
+
+def test_append_refuses_other_numbers_of_requests(gdn):
+    """k [B, T, heads, D] and slots [B]: tokens are not dealt out anew to another number of slots."""
+    c = Case(33, [20, 20, 20, 20], H=2, Hq=2)
+    new = torch.randn(2, 4, 2, 64, device="cuda").to(BF16)
+    k, v = c.to(c.k), c.to(c.v)
+    k0, v0 = k.clone(), v.clone()
+    args = c.to(c.table), c.to(c.seq), c.to(c.slots)
+    with pytest.raises(ValueError, match="requests"):
+        gdn.gdn_kv_append(new, new, k, v, *args)
+    assert torch.equal(k, k0) and torch.equal(v, v0)
+    # packed tokens, and with offsets any grouping, are not such
+    gdn.gdn_kv_append(new.reshape(8, 2, 64), new.reshape(8, 2, 64), k, v, *args)
+    k1, v1 = k0.clone(), v0.clone()
+    gdn.gdn_kv_append(new.reshape(1, 8, 2, 64), new.reshape(1, 8, 2, 64), k1, v1, *args)
+    assert torch.equal(k, k1) and torch.equal(v, v1) and not torch.equal(k, k0)
+    k1, v1 = k0.clone(), v0.clone()
+    off = torch.tensor([0, 2, 4, 6, 8], dtype=torch.int32, device="cuda")
+    gdn.gdn_kv_append(new, new, k1, v1, *args, off)
+    assert torch.equal(k, k1) and torch.equal(v, v1)
