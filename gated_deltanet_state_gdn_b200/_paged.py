@@ -289,18 +289,22 @@ def _table(block_table, ref_count, seq_lens, page_size):
 
 
 def _pools(pools, rows, device):
-    """The arrays of a call: dimension 0 counts pages (or slots), the others are one dense block."""
+    """The arrays of a call: dimension 0 counts pages (or slots), the others are one dense block.
+    Arrays without elements (windows of a conv of one tap) have nothing to copy."""
     if isinstance(pools, torch.Tensor):
         raise TypeError("pools must be a list of tensors")
     if not pools:
         return None, 0
     out = (_Pool * len(pools))()
+    count = 0
     for i, t in enumerate(pools):
         if not isinstance(t, torch.Tensor) or t.device != device or t.dim() < 1:
             raise TypeError(f"pools[{i}] must be a tensor on {device}")
         if t.shape[0] != rows:
             raise ValueError(f"pools[{i}] must have {rows} rows, got {t.shape[0]}")
         n = t.numel() // rows
+        if n == 0:
+            continue
         if not t.is_contiguous():
             dense = 1           # the axes of a row, from the innermost, without holes
             for st, sz in sorted((s, z) for s, z in zip(t.stride()[1:], t.shape[1:]) if z > 1):
@@ -308,8 +312,9 @@ def _pools(pools, rows, device):
                     raise ValueError(f"the rows of pools[{i}] must be dense")
                 dense *= sz
         stride = t.stride(0) if rows > 1 else n
-        out[i] = _Pool(t.data_ptr(), stride * t.element_size(), n * t.element_size())
-    return out, len(pools)
+        out[count] = _Pool(t.data_ptr(), stride * t.element_size(), n * t.element_size())
+        count += 1
+    return out, count
 
 
 @_on_stream("block_table")

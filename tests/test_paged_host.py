@@ -354,6 +354,18 @@ def test_pool_rows():
         _pools(kv, 5, dev)
 
 
+def test_pools_without_elements():
+    """The window pool of a conv of one tap, [slots, channels, 0], is taken and left out."""
+    from gated_deltanet_state_gdn_b200._paged import _pools
+    dev = torch.device("cpu")
+    x, y = torch.zeros(5, 4), torch.zeros(5, 7)
+    arr, n = _pools([torch.zeros(5, 64, 0), x, torch.zeros(5, 0), y], 5, dev)
+    assert n == 2 and [arr[i].data for i in range(2)] == [x.data_ptr(), y.data_ptr()]
+    assert _pools([torch.zeros(5, 64, 0)], 5, dev)[1] == 0
+    with pytest.raises(ValueError, match="rows"):
+        _pools([torch.zeros(4, 64, 0)], 5, dev)
+
+
 # ---------------------------------------------------------------- the models themselves
 def test_model_of_attention():
     """Against torch's own softmax on whole rows, and a window and a cut by hand."""
