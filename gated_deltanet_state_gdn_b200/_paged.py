@@ -351,8 +351,9 @@ def gdn_page_fork(block_table, ref_count, seq_lens, parents, children, page_size
 
     Tables as for gdn_page_resize, updated in place; parents, children: [n] int32 (negative:
     padding); pools: the tensors whose dimension 0 counts slots (the state pools of gdn_decode,
-    the windows of gdn_conv1d): row child becomes a copy of row parent.  What a child held is
-    given back.  Returns (block_table, ref_count, seq_lens).
+    the windows of gdn_conv1d), the rest of each one dense block (of a state pool with padded
+    heads pass the heads, ``pool.unbind(1)``): row child becomes a copy of row parent.  What a
+    child held is given back.  Returns (block_table, ref_count, seq_lens).
     """
     device = block_table.device
     t, rows, num_pages = _table(block_table, ref_count, seq_lens, page_size)
