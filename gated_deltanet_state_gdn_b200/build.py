@@ -7,9 +7,10 @@ time (the driver entry points it uses are fetched at run time), so it loads on
 a machine without a GPU for the symbol checks.
 
 --checked builds libgdn_checked.so instead: the same sources compiled with
-GDN_CHECKS, where every global access and every data-dependent shared-memory
-access is tested against its buffer first (an access outside it is skipped and
-GDN_DEV_BOUNDS set in the status word).  It is a test build, slower than the
+GDN_CHECKS, where every global access (but for walks over a list by its own
+length, and boxes of a tensor map, which the hardware bounds) and every
+data-dependent shared-memory access is tested against its buffer first (an
+access outside it is skipped and GDN_DEV_BOUNDS set in the status word).  It is a test build, slower than the
 product library; --all builds both.
 """
 from __future__ import annotations

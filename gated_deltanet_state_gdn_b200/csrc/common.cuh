@@ -78,7 +78,8 @@ __device__ __forceinline__ float softplus20(float x)
 __device__ __forceinline__ float sigmoidf_(float x) { return 1.0f / (1.0f + expf(-x)); }
 
 // ---------------------------------------------------------------- checked builds
-// Compiled with GDN_CHECKS, every global access and every data-dependent shared-memory access
+// Compiled with GDN_CHECKS, every global access (but for walks over a list by its own length, and
+// boxes of a tensor map, which the hardware bounds) and every data-dependent shared-memory access
 // is first tested against its buffer; one outside it is skipped (a load yields zero) and
 // GDN_DEV_BOUNDS is OR-ed into the status word.  Without GDN_CHECKS the tests are constant
 // true and vanish.

@@ -64,6 +64,7 @@ __device__ __forceinline__ uint2 quantise(const uint4 &w, bool bf16, float scale
 __device__ int64_t place(const GdnAppendArgs &a, int64_t n, const int32_t *offsets)
 {
     const gdn_paged_cache &kv = a.cache;
+    int32_t *const status = a.dev_status;
     int b;
     int64_t end;
     if (offsets) {
@@ -72,12 +73,13 @@ __device__ int64_t place(const GdnAppendArgs &a, int64_t n, const int32_t *offse
         int lo = 0, hi = a.B;        // offsets[lo] <= n < offsets[hi], were they sentinels
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if (offsets[mid] <= n)
+            if (in_range(mid, 1, a.B + 1, status) && offsets[mid] <= n)
                 lo = mid;
             else
                 hi = mid;
         }
         b = lo;
+        if (!in_range(b, 2, a.B + 1, status)) return -1;
         if (n < offsets[b]) return -1;    // ahead of the first request
         end = offsets[b + 1];
         if (end > a.N) end = a.N;
@@ -87,6 +89,7 @@ __device__ int64_t place(const GdnAppendArgs &a, int64_t n, const int32_t *offse
         b = (int)n / T;
         end = (int64_t)(b + 1) * T;
     }
+    if (!in_range(b, 1, a.B, status)) return -1;
     const int slot = a.slots ? __ldg(a.slots + b) : b;
     if (slot < 0) return -1;
     int bad = 0;
@@ -99,6 +102,7 @@ __device__ int64_t place(const GdnAppendArgs &a, int64_t n, const int32_t *offse
             bad = GDN_DEV_BAD_LENGTH;
         } else {
             const int pg = (int)((uint32_t)pos / (uint32_t)kv.page_size);
+            if (!in_range(pg, 1, kv.width, status)) return -1;
             const int id = __ldg(kv.block_table + slot * kv.table_stride + pg);
             if ((uint32_t)id < (uint32_t)kv.num_pages)
                 at = id * kv.page_stride + (pos - (int64_t)pg * kv.page_size) * kv.token_stride;
@@ -106,7 +110,7 @@ __device__ int64_t place(const GdnAppendArgs &a, int64_t n, const int32_t *offse
                 bad = GDN_DEV_BAD_PAGE;
         }
     }
-    if (bad && a.dev_status) atomicOr(a.dev_status, bad);
+    if (bad && status) atomicOr(status, bad);
     return at;
 }
 
@@ -153,15 +157,17 @@ kv_append_kernel(const __grid_constant__ GdnAppendArgs a, const int tokens, cons
             const bool mine = col < per_token && t0 < side;
             const int v = col >= kv.heads * D8, r = col - (v ? kv.heads * D8 : 0), h = r / D8, d = (r - h * D8) * 8;
             const int64_t ts = v ? a.v_token_stride : a.k_token_stride;
-            const uint16_t *x = static_cast<const uint16_t *>(v ? a.v : a.k) + (n0 + t0) * ts +
-                                h * (v ? a.v_head_stride : a.k_head_stride) + d;
+            const int64_t hs = v ? a.v_head_stride : a.k_head_stride;
+            const uint16_t *const x0 = static_cast<const uint16_t *>(v ? a.v : a.k);
+            const uint16_t *x = x0 + (n0 + t0) * ts + h * hs + d;
+            const int64_t x_n = (a.N - 1) * ts + (kv.heads - 1) * hs + kv.head_dim;
             const int64_t off = h * kv.head_stride + d;
             unsigned char *const y = static_cast<unsigned char *>(v ? kv.v : kv.k) + off * (E4M3 ? 1 : 2);
             float scale = 1.f, inv = 1.f;
             uint32_t flip = 0u;
             if (E4M3 && mine) {
                 const float *const sc = v ? kv.v_scale : kv.k_scale;
-                if (sc) scale = __ldg(sc + h);
+                if (sc && in_range(h, 1, kv.heads, a.dev_status)) scale = __ldg(sc + h);
                 if (signbit(scale)) flip = 0x80808080u;
                 scale = fabsf(scale);
                 inv = __frcp_rn(scale);
@@ -173,7 +179,9 @@ kv_append_kernel(const __grid_constant__ GdnAppendArgs a, const int tokens, cons
                 uint4 w[kHold];
 #pragma unroll
                 for (int k = 0; k < kHold; ++k) {
-                    if (mine && i + k * side < here) w[k] = __ldcs(reinterpret_cast<const uint4 *>(x));
+                    if (mine && i + k * side < here)
+                        w[k] = in_range(x - x0, 8, x_n, a.dev_status) ? __ldcs(reinterpret_cast<const uint4 *>(x))
+                                                                      : make_uint4(0u, 0u, 0u, 0u);
                     x += side * ts;
                 }
                 if (c0 == 0 && i == t0) __syncthreads();        // the places are known

@@ -154,6 +154,12 @@ __device__ __forceinline__ RowInfo row_info(const GdnAttnArgs &a, int b, bool te
     return r;
 }
 
+// elements from the first to past the last of q
+__device__ __forceinline__ int64_t q_elements(const GdnAttnArgs &a)
+{
+    return ((int64_t)a.B * a.T - 1) * a.q_token_stride + (a.Hq - 1) * a.q_head_stride + a.cache.head_dim;
+}
+
 // first position that some token of the request sees
 __device__ __forceinline__ int first_seen(const GdnAttnArgs &a, int len)
 {
@@ -429,8 +435,10 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                 const int n = min(C::RMAX, rows_all - r0) * lines;
                 for (int k = fw * 32 + lane; k < n; k += C::FETCH * 32) {
                     const int r = r0 + k / lines, t = r / group;
-                    touch_l1(static_cast<const uint16_t *>(a.q) + ((int64_t)cb * a.T + t) * a.q_token_stride +
-                             (int64_t)(h * group + r - t * group) * a.q_head_stride + (k % lines) * 64);
+                    const uint16_t *const line =
+                        static_cast<const uint16_t *>(a.q) + ((int64_t)cb * a.T + t) * a.q_token_stride +
+                        (int64_t)(h * group + r - t * group) * a.q_head_stride + (k % lines) * 64;
+                    if (in_range(line - static_cast<const uint16_t *>(a.q), 2, q_elements(a), a.dev_status)) touch_l1(line);
                 }
             }
             // the next place of the run (past the last one the cursor may stand anywhere)
@@ -510,6 +518,8 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         if (!wait_phase(full0 + 8 * st, (i / kStages) & 1, &s_abort, a.dev_status)) break;
         const Desc d = s_desc[st];
         const int h = d.h, rt = d.rt;
+        if constexpr (gdn::kChecked)        // of the request, and of the heads (and their scales)
+            if (!in_range(d.b, 1, a.B, a.dev_status) || !in_range(h, 1, H, a.dev_status)) break;
 
         if (i == 0 || d.tile == 0) {        // a unit begins: its query rows
             seg_tile = d.tile;
@@ -527,6 +537,9 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                 qr[e] = reinterpret_cast<const uint32_t *>(
                     static_cast<const uint16_t *>(a.q) + ((int64_t)d.b * a.T + t) * a.q_token_stride +
                     (int64_t)(h * group + g) * a.q_head_stride);
+                if constexpr (gdn::kChecked)
+                    has[e] = has[e] && in_range(reinterpret_cast<const uint16_t *>(qr[e]) - static_cast<const uint16_t *>(a.q),
+                                                D, q_elements(a), a.dev_status);
                 const int64_t pos = (int64_t)d.len - a.T + t;
                 hi[e] = has[e] ? (int)pos : -1;
                 lo[e] = has[e] && a.window > 0 && pos >= a.window ? (int)(pos - a.window) : -1;
@@ -982,7 +995,11 @@ paged_attn_join_kernel(const GdnAttnArgs a, const int RT, const int RMAX, const 
         return ((int64_t)sp.b * a.T + t) * a.Hq + h * group + r - t * group;
     };
     // part k: the first block's is its second, the others' are their first
-    auto at = [&](int k, int rl) { return ((int64_t)(sp.c0 + k) * 2 + (k == 0 ? 1 : 0)) * RMAX + rl; };
+    // (a checked build reads the first row for one that is none)
+    auto at = [&](int k, int rl) {
+        const int64_t row = ((int64_t)(sp.c0 + k) * 2 + (k == 0 ? 1 : 0)) * RMAX + rl;
+        return in_range(row, 1, (int64_t)blocks * 2 * RMAX, a.dev_status) ? row : 0;
+    };
     auto store = [&](int64_t row, int d, float4 y, float sum) {
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
         uint32_t *const out = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.out) + row * D + d);

@@ -127,7 +127,7 @@ __device__ __forceinline__ int warps_scan(int x, int *s_warp, int *total)
 }
 
 // copy piece `item` of row src to row dst
-__device__ __forceinline__ void copy_piece(const Pools &ps, int item, int64_t src, int64_t dst)
+__device__ __forceinline__ void copy_piece(const Pools &ps, int item, int64_t src, int64_t dst, int32_t *status)
 {
     int lo = 0, hi = ps.n - 1;          // the last pool whose first piece is <= item
     while (lo < hi) {
@@ -137,6 +137,7 @@ __device__ __forceinline__ void copy_piece(const Pools &ps, int item, int64_t sr
     const Pool &p = ps.p[lo];
     const int64_t at = (int64_t)(item - p.first) * kCopyBytes;
     const int64_t n = p.bytes - at < kCopyBytes ? p.bytes - at : kCopyBytes;
+    if (!in_range(at, n, p.bytes, status)) return;
     const unsigned char *const s = p.data + src * p.stride + at;
     unsigned char *const d = p.data + dst * p.stride + at;
     const int tid = threadIdx.x;
@@ -177,7 +178,7 @@ __device__ __noinline__ void rename_rows(const gdn_page_table &t, const int32_t 
         int32_t *const e = t.block_table + s * t.table_stride;
         const int had = pages_of(len, t.page_size);
         for (int j = lane; j < had; j += 32) {
-            const int id = e[j];
+            const int id = in_range(j, 1, t.width, status) ? e[j] : -1;
             const int to = (uint32_t)id < (uint32_t)t.num_pages ? __ldcg(map + id) : -1;
             if (to < 0)
                 tell(status, GDN_DEV_BAD_PAGE);
@@ -198,7 +199,7 @@ copy_pairs_kernel(const __grid_constant__ Pools ps, const int2 *pairs, const int
     for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
         const int2 p = pairs[i / ps.pieces];
         if (in_range(p.x, 1, num_rows, status) && in_range(p.y, 1, num_rows, status))
-            copy_piece(ps, (int)(i % ps.pieces), p.x, p.y);
+            copy_piece(ps, (int)(i % ps.pieces), p.x, p.y, status);
     }
     if (map) rename_rows(t, map, status);
 }
@@ -353,7 +354,7 @@ resize_kernel(const __grid_constant__ gdn_page_table t, const int32_t *row_list,
             Row x;
             if (i < n) {
                 x = rows[i];
-                if (x.row >= 0 && x.copied) {
+                if (x.row >= 0 && x.copied && in_range(x.had - 1, 1, t.width, status)) {
                     x.last = __ldcg(t.block_table + x.row * t.table_stride + x.had - 1);
                     if ((uint32_t)x.last >= (uint32_t)t.num_pages) {
                         if (rank == 0) tell(status, GDN_DEV_BAD_PAGE);
@@ -439,7 +440,7 @@ resize_kernel(const __grid_constant__ gdn_page_table t, const int32_t *row_list,
         copies += sum;
         if (rank == 0 && i < n && x.row >= 0) {
             t.seq_lens[x.row] = x.len;
-            if (copy) {
+            if (copy && in_range(k, 1, n, status) && in_range(x.first, 1, t.num_pages, status)) {
                 atomicSub(t.ref_count + x.last, 1);
                 ws.pairs[k] = make_int2(x.last, __ldcg(ws.free_list + x.first));
             }
@@ -456,12 +457,13 @@ resize_kernel(const __grid_constant__ gdn_page_table t, const int32_t *row_list,
 #pragma unroll
             for (int k = 0; k < kChunk / 32; ++k) {
                 const int j = j00 + k * 32 + lane;
-                id[k] = j < x.need && in_range(x.had - x.copied + j, 1, t.width, status)
+                id[k] = j < x.need && in_range(x.had - x.copied + j, 1, t.width, status) &&
+                                in_range(x.first + j, 1, t.num_pages, status)
                             ? __ldcg(ws.free_list + x.first + j) : -1;
             }
 #pragma unroll
             for (int k = 0; k < kChunk / 32; ++k)
-                if (id[k] >= 0) {
+                if (id[k] >= 0 && in_range(id[k], 1, t.num_pages, status)) {
                     e[j00 + k * 32 + lane] = id[k];
                     t.ref_count[id[k]] = 1;
                 }
@@ -541,7 +543,9 @@ compact_kernel(const __grid_constant__ gdn_page_table t, int32_t *const map, con
     const int below = U < P ? __ldcg(ws.count + 1) : U;     // used pages of number < U
     const int moves = U - below;
     for (int k = rank * kThreads + tid; k < moves; k += blocks * kThreads) {
+        if (!in_range(below + k, 1, P, status)) continue;
         const int src = __ldcg(ws.used + below + k), dst = __ldcg(ws.open + k);
+        if (!in_range(src, 1, P, status) || !in_range(dst, 1, P, status)) continue;
         t.ref_count[dst] = __ldcg(t.ref_count + src);
         t.ref_count[src] = 0;
         map[src] = dst;
@@ -581,7 +585,7 @@ fork_kernel(const __grid_constant__ Pools ps, const gdn_page_table t, const int3
             continue;
         }
         if (!table) {
-            copy_piece(ps, (int)((i - table_blocks) % ps.pieces), p, c);
+            copy_piece(ps, (int)((i - table_blocks) % ps.pieces), p, c, status);
             continue;
         }
         const int old = *reinterpret_cast<const volatile int32_t *>(t.seq_lens + c);

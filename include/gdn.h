@@ -92,9 +92,10 @@ enum {
     GDN_DEV_BAD_SLOT = 1,  /* a slot index >= the pool size was skipped (decode, conv1d) */
     GDN_DEV_TIMEOUT = 2,   /* a kernel-internal wait exceeded its bound; outputs invalid */
     GDN_DEV_INTERNAL = 4,  /* a kernel's layout self-check failed; nothing was computed */
-    /* Checked builds only (libgdn_checked.so, compiled with GDN_CHECKS): every global and
-     * data-dependent shared-memory access is tested against its buffer first; one outside it
-     * is skipped (a load reads zero) and this bit is set.  Ordinary builds never set it. */
+    /* Checked builds only (libgdn_checked.so, compiled with GDN_CHECKS): every global (but for
+     * walks over a list by its own length) and data-dependent shared-memory access is tested
+     * against its buffer first; one outside it is skipped (a load reads zero) and this bit is
+     * set.  Ordinary builds never set it. */
     GDN_DEV_BOUNDS = 8,
     GDN_DEV_BAD_PAGE = 16,    /* a page that a row's length needs is not in [0, num_pages) */
     GDN_DEV_BAD_LENGTH = 32,  /* a length outside what a row of the page table holds */
