@@ -59,36 +59,61 @@ __device__ __forceinline__ uint2 quantise(const uint4 &w, bool bf16, float scale
     return make_uint2(out[0] ^ flip, out[1] ^ flip);
 }
 
-// where token n goes: element offset of its head 0 in the cache, or -1; `offsets` are the row
-// offsets in global or shared memory
-__device__ int64_t place(const GdnAppendArgs &a, int64_t n, const int32_t *offsets)
+// The request with s <= n < e among the offsets, or -1.  Where they ascend, which is how they are
+// searched, it is the last whose s is <= n (empty requests before it end at or before n).
+__device__ int request_of(const GdnAppendArgs &a, int64_t n, const int32_t *offsets)
+{
+    int lo = 0, hi = a.B;        // offsets[lo] <= n < offsets[hi], were they sentinels
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (in_range(mid, 1, a.B + 1, a.dev_status) && offsets[mid] <= n)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return in_range(lo, 2, a.B + 1, a.dev_status) && offsets[lo] <= n && n < offsets[lo + 1] ? lo : -1;
+}
+
+// The same, by a whole warp for a token (or none: n < 0) each, where offsets may fall back, as those
+// do behind the last one in use of a list of fixed size: what is empty then may lead the search
+// astray, which it shows by finding nothing.  Offsets in shared memory (`own`) are raised to the
+// largest up to each, which leaves every other request what it is; others are gone through.
+__device__ int warp_request_of(const GdnAppendArgs &a, int64_t n, const int32_t *offsets, int32_t *own, int &falls)
+{
+    const int lane = threadIdx.x & 31;
+    int b = n >= 0 ? request_of(a, n, offsets) : -1;
+    if (!__any_sync(0xffffffffu, n >= 0 && b < 0)) return b;
+    if (falls < 0) {             // not known yet
+        bool down = false;
+        for (int i = lane; i < a.B; i += 32) down = down || offsets[i] > offsets[i + 1];
+        falls = __any_sync(0xffffffffu, down);
+    }
+    if (!falls) return b;        // ahead of the first request or behind the last one
+    if (own) {
+        int top = own[0];
+        for (int i0 = 0; i0 <= a.B; i0 += 32) {
+            const int i = i0 + lane;
+            int x = i <= a.B ? max(own[i], top) : top;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) x = max(x, __shfl_up_sync(0xffffffffu, x, d));
+            if (i <= a.B) own[i] = x;
+            top = __shfl_sync(0xffffffffu, x, 31);
+        }
+        __syncwarp();
+        falls = 0;
+        return n >= 0 && b < 0 ? request_of(a, n, own) : b;
+    }
+    for (int k = 0; n >= 0 && b < 0 && k < a.B; ++k)
+        if (offsets[k] <= n && n < offsets[k + 1]) b = k;
+    return b;
+}
+
+// where token n of request b goes: element offset of its head 0 in the cache, or -1
+__device__ int64_t place(const GdnAppendArgs &a, int64_t n, int b, const int32_t *offsets)
 {
     const gdn_paged_cache &kv = a.cache;
     int32_t *const status = a.dev_status;
-    int b;
-    int64_t end;
-    if (offsets) {
-        // The request with s <= n < e; offsets ascend, so it is the last whose s is <= n (empty
-        // requests before it end at or before n).
-        int lo = 0, hi = a.B;        // offsets[lo] <= n < offsets[hi], were they sentinels
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (in_range(mid, 1, a.B + 1, status) && offsets[mid] <= n)
-                lo = mid;
-            else
-                hi = mid;
-        }
-        b = lo;
-        if (!in_range(b, 2, a.B + 1, status)) return -1;
-        if (n < offsets[b]) return -1;    // ahead of the first request
-        end = offsets[b + 1];
-        if (end > a.N) end = a.N;
-        if (n >= end) return -1;          // behind the last one
-    } else {
-        const int T = (int)(a.N / a.B);
-        b = (int)n / T;
-        end = (int64_t)(b + 1) * T;
-    }
+    const int64_t end = offsets ? min((int64_t)offsets[b + 1], a.N) : (int64_t)(b + 1) * (a.N / a.B);
     if (!in_range(b, 1, a.B, status)) return -1;
     const int slot = a.slots ? __ldg(a.slots + b) : b;
     if (slot < 0) return -1;
@@ -131,10 +156,13 @@ kv_append_kernel(const __grid_constant__ GdnAppendArgs a, const int tokens, cons
             for (int i = lane; i <= a.B; i += 32) s_offsets[i] = __ldg(a.row_offsets + i);
         __syncwarp();
         const int32_t *const offsets = staged ? s_offsets : a.row_offsets;
-        int buf = 0;
+        const int each = (int)(a.N / a.B);      // tokens a request, without offsets
+        int buf = 0, falls = -1;
         for (int64_t chunk = blockIdx.x; chunk < chunks; chunk += gridDim.x, buf ^= 1) {
             // (the chunk before the last one has been copied: the others are past its meeting)
-            if (lane < size_of(chunk)) s_at[buf][lane] = place(a, chunk * tokens + lane, offsets);
+            const int64_t n = lane < size_of(chunk) ? chunk * tokens + lane : -1;
+            const int b = !offsets ? (int)n / each : warp_request_of(a, n, offsets, staged ? s_offsets : nullptr, falls);
+            if (n >= 0) s_at[buf][lane] = b < 0 ? -1 : place(a, n, b, offsets);
             __syncthreads();
         }
         return;

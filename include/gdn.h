@@ -408,8 +408,8 @@ typedef struct {
  * gdn_kv_append -- write new tokens' keys and values to the pages of their positions.
  *
  * Request b of B has the tokens [s, e) = [row_offsets[b], row_offsets[b+1]) of k and v (clamped
- * to [0, N]; e <= s is empty), or with row_offsets NULL the tokens [b*N/B, (b+1)*N/B).  They
- * are the last e - s positions of row slots[b] of the cache, whose seq_lens entry counts them
+ * to [0, N]; e <= s is empty, and no two requests have a token in common), or with row_offsets
+ * NULL the tokens [b*N/B, (b+1)*N/B).  They are the last e - s positions of row slots[b] of the cache, whose seq_lens entry counts them
  * already: token s + i goes to position seq_lens[slot] - (e - s) + i.
  *   16-bit cache   the values are stored as they are (k, v and the cache have one type);
  *   GDN_E4M3       round(clamp(x / scale[h], -448, 448)) to the nearest of the type's numbers,

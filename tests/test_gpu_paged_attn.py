@@ -424,3 +424,42 @@ def test_append_refuses_other_numbers_of_requests(gdn):
     off = torch.tensor([0, 2, 4, 6, 8], dtype=torch.int32, device="cuda")
     gdn.gdn_kv_append(new, new, k1, v1, *args, off)
     assert torch.equal(k, k1) and torch.equal(v, v1)
+
+
+@pytest.mark.parametrize("B", [5, 40, 300, 1023, 1024, 2500])
+@pytest.mark.parametrize("tail", ["zeros", "past", "short"])
+def test_append_offsets_with_a_tail(gdn, B, tail):
+    """A list of offsets of fixed size of which only the first entries are in use: those behind fall
+    back to zero, or stand past N (both are empty requests), or N goes further than the last."""
+    live, T, H, D, page = max(2, B // 3), 2, 2, 64, 16
+    g = torch.Generator().manual_seed(B)
+    counts = torch.randint(0, 4, (live,), generator=g)
+    n = int(counts.sum())
+    off = torch.zeros(B + 1, dtype=torch.int64)
+    off[1:live + 1] = torch.cumsum(counts, 0)
+    N = n + 70
+    off[live + 1:] = {"zeros": 0, "past": N + 5, "short": n}[tail]
+    if tail == "past":              # the last live request ends where the tokens do
+        counts[-1] += N - n
+        off[live] = N
+    seq = torch.zeros(B, dtype=torch.int32)
+    seq[:live] = counts + 3
+    width = pages_of(int(seq.max()), page)
+    table = torch.arange(B * width, dtype=torch.int32).reshape(B, width)
+    slots = torch.randperm(B, generator=g).to(torch.int32)
+    by_slot = torch.empty_like(seq)
+    by_slot[slots.long()] = seq
+    kv = torch.randn(N, 2 * H, D, generator=g).to(BF16)
+    k, v = (torch.zeros(B * width, page, H, D, dtype=BF16, device="cuda") for _ in range(2))
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    packed = kv.cuda()
+    gdn.gdn_kv_append(packed[:, :H], packed[:, H:], k, v, table.cuda(), by_slot.cuda(), slots.cuda(),
+                      off.to(torch.int32).cuda(), dev_status=st)
+    wk, wv = (torch.zeros(B * width, page, H, D, dtype=BF16) for _ in range(2))
+    at = 0
+    for b in range(live):
+        for i in range(int(counts[b])):
+            p = int(table[int(slots[b]), (3 + i) // page])
+            wk[p, (3 + i) % page], wv[p, (3 + i) % page] = kv[at, :H], kv[at, H:]
+            at += 1
+    assert torch.equal(k.cpu(), wk) and torch.equal(v.cpu(), wv) and int(st.item()) == 0
