@@ -311,7 +311,7 @@ resize_kernel(const __grid_constant__ gdn_page_table t, const int32_t *row_list,
     __syncthreads();
     const int most_gone = s_most[0], most_new = s_most[1];
     // a wide table of which little changes (a step of decoding): the first block does it alone
-    if (blocks > 1 && t.num_pages <= kThreads * kPer && (int64_t)n * (most_gone + most_new) <= kFewEntries) {
+    if (blocks > 1 && t.num_pages <= kThreads * kPer && n * ((int64_t)most_gone + most_new) <= kFewEntries) {
         if (rank > 0) return;
         blocks = 1;
     }
