@@ -6,14 +6,15 @@
 // and out = O / l.  Two parts (m1, l1, O1), (m2, l2, O2) of one row join by the same rule, which
 // is what lets the tokens of a row be cut anywhere.
 //
-// What bounds it: every key and value is read once and meets T Hq / H rows, 2 T Hq / H
-// operations a byte in 16 bits; up to 16 rows a head HBM is the bound, and warp mma keeps up with
-// the tensor pipe 18 % busy, so tcgen05 (64 or 128 rows, of which one token's group would fill 1
-// to 16) is not used.  Measured on a B200 (copy rate 6.46 TB/s): 243 rows of 1 to 4096 tokens, 32
-// heads on 8 of 128, bf16: 308 to 321 us, 6.4 to 6.6 TB/s; over e4m3 194 us, 5.3 TB/s, where the steps of the
-// computing warps (conversions, warp mma) are nearly as long as the memory's; one row of 131072,
-// 16 heads on 2 of 256, fp16: 55 us, 4.9 TB/s, 10 us of them start and join; 16 tokens a row of
-// the first case (64 rows a head): 631 us, bound by the rate of warp mma, 206 TFLOP/s.
+// What bounds it: a key or value meets T Hq / H rows, T Hq / H operations a byte in 16 bits, and is
+// read once for every 64 of them (32 where heads are wider than 128).  Up to 16 rows a head HBM is
+// the bound, and warp mma keeps up with the tensor pipe 18 % busy, so tcgen05 (64 or 128 rows, of
+// which one token's group would fill 1 to 16) is not used.  Measured on a B200 (copy rate 6.46
+// TB/s): 243 rows of 1 to 4096 tokens, 32 heads on 8 of 128, bf16: 308 to 322 us, 6.3 to 6.6 TB/s;
+// over e4m3 195 us, 5.3 TB/s, where the steps of the computing warps (conversions, warp mma) are
+// nearly as long as the memory's; one row of 131072, 16 heads on 2 of 256, fp16: 55 us, 4.9 TB/s,
+// 10 us of them start and join; 16 tokens a row of the first case (64 rows a head): 631 us, bound by
+// the rate of warp mma, 206 TFLOP/s.
 //
 // Layout of the work.
 //   - A unit is (request, head, block of 16 WR rows); its tokens are cut into tiles of 16 KB of

@@ -9,8 +9,10 @@
 // the order of the lists and of the page numbers, so a call has one result; atomics only count
 // integers.
 // Measured on a B200: 40000 pages of 64 KB in order, half used: 427 us, 6.15 TB/s of 6.46 (copy
-// rate); 64 children of 16 requests with 6.5 MB of states each: 115 us with their growth; a
-// decoding step's growth of 256 rows 8 us; 262144 pages given back and as many handed out 33 us.
+// rate); 64 children of 16 requests with 6.4 MB of states each: 115 us with their growth, of which the
+// states take 107 (80 were each parent read once from HBM: its children, pieces apart, make that twice);
+// a decoding step's growth of 256 rows 8 to 11 us on up to 16384 pages, which one block passes over at
+// once, and 20 us on 300000; 262144 pages given back and as many handed out 33 us.
 #include <cooperative_groups.h>
 
 #include "cache.cuh"
