@@ -257,8 +257,8 @@ def gdn_paged_attn(q, k_cache, v_cache, block_table, seq_lens, slots=None, *, sc
     if lse is not None:
         _tensor("lse", lse, torch.float32, (B, T, Hq), device)
     elif return_lse:
-        lse = torch.full((B, T, Hq), -math.inf, device=device) if out is not None else \
-            q.new_empty((B, T, Hq), dtype=torch.float32)
+        lse = torch.full((B, T, Hq), -math.inf, dtype=torch.float32, device=device) \
+            if out is not None else q.new_empty((B, T, Hq), dtype=torch.float32)
     if out is not None:
         _tensor("out", out, q.dtype, (B, T, Hq, D), device)
     elif flags:

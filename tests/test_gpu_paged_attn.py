@@ -398,6 +398,22 @@ def test_append_rounds_to_the_same_bytes(gdn, dtype, scale):
         np.testing.assert_array_equal(got, bytes_of(wide(y), scale or 1.0))
 
 
+@pytest.mark.parametrize("default", [torch.bfloat16, torch.float64])
+def test_other_default_types(gdn, default):
+    """What a call makes is of the types that it says, whatever torch's default type is."""
+    c = Case(35, [5, 40, 0, 7], pad=(1,), T=2)
+    want, wl = c.attend(gdn)
+    out, lse = torch.empty_like(want), torch.empty_like(wl)
+    torch.set_default_dtype(default)
+    try:
+        got = [c.attend(gdn), c.attend(gdn, out=out.zero_()), c.attend(gdn, lse=lse.fill_(-math.inf))]
+    finally:
+        torch.set_default_dtype(torch.float32)
+    for o, x in got:
+        assert o.dtype == BF16 and x.dtype == torch.float32
+        assert torch.equal(o, want) and torch.equal(x, wl)
+
+
 def test_windows_past_32_bits(gdn):
     c = Case(32, [70, 40, 300], T=2)
     want = c.attend(gdn)
