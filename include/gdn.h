@@ -427,8 +427,10 @@ typedef struct {
  * Requirements: D a multiple of 8 (GDN_E4M3: of 16) and at most 256; k, v and the cache
  * 16-byte aligned with strides that are multiples of 16 bytes (8 elements for k and v); the
  * strides of the cache keep its vectors apart, and no key shares bytes with a value
- * (GDN_ERR_ALIAS; values may lie in the gaps between keys).  Requests name distinct rows.
- * Nothing else of the cache is touched.
+ * (GDN_ERR_ALIAS; values may lie in the gaps between keys).  Requests name distinct rows, and
+ * the pages they write to are held by no other (gdn_page_resize sees to that for the positions
+ * that a row gains; tokens written anew into a page that a fork shares are written for all its
+ * holders).  Nothing else of the cache is touched.
  */
 GDN_API gdn_status gdn_kv_append(const void *k, const void *v, int64_t k_token_stride,
                                  int64_t k_head_stride, int64_t v_token_stride,

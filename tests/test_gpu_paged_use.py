@@ -330,3 +330,50 @@ def test_attention_wait_runs_out_on_request(gdn):
         gdn.use_library(product)
     assert same(got, want)
     check_attend(c, got, attend(c))
+
+
+def test_first_calls_inside_a_capture(gdn):
+    """A program whose first calls are captured, without one before: what a call sets up on the device
+    it can set up there."""
+    import os
+    import subprocess
+    import sys
+    code = """if 1:
+        import sys
+        sys.path[:0] = ["tests", "."]
+        import torch
+        import gated_deltanet_state_gdn_b200 as gdn
+        from test_gpu_paged_use import Server, ints, same
+        a, b = Server(1), Server(1)
+        wide = [torch.full((6, 40000), -1, dtype=torch.int32, device="cuda") for _ in range(2)]
+        refs = [ints([0] * 70000) for _ in range(2)]        # (planned by a cluster)
+        seqs = [ints([0] * 6) for _ in range(2)]
+        long = ints([9000, 1, 20000, 7, 0, 5])
+
+        def turn(s, i):
+            s.start(gdn)
+            gdn.gdn_page_fork(s.table, s.ref, s.seq, ints_[0], ints_[1], s.page, dev_status=s.status)
+            gdn.gdn_page_resize(s.table, s.ref, s.seq, s.rows, grown, s.page, [s.k, s.v], dev_status=s.status)
+            gdn.gdn_kv_append(s.kn, s.vn, s.k, s.v, s.table, s.seq, s.slots, dev_status=s.status)
+            gdn.gdn_paged_attn(s.q, s.k, s.v, s.table, s.seq, s.slots, out=s.out, dev_status=s.status)
+            gdn.gdn_page_resize(wide[i], refs[i], seqs[i], s.rows, long, 1, dev_status=s.status)
+            return (gdn.gdn_page_compact(s.table, s.ref, s.seq, s.page, [s.k, s.v], dev_status=s.status),
+                    gdn.gdn_page_compact(wide[i], refs[i], seqs[i], 1, dev_status=s.status))
+
+        ints_ = ints([2, 5]), ints([0, 1])
+        grown = ints([42, 92, 42, 5, 66, 92])               # two tokens more each: shared pages are copied
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            to = turn(a, 0)
+        graph.replay()
+        want = turn(b, 1)
+        torch.cuda.synchronize()
+        assert same(a.everything(), b.everything()) and same(to, want)
+        assert same([wide[0], refs[0], seqs[0]], [wide[1], refs[1], seqs[1]]) and int(seqs[0].sum()) == 29013
+        assert int(a.status.item()) == 0
+        print("replayed")
+    """
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "replayed" in r.stdout, r.stdout + r.stderr
