@@ -436,10 +436,13 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                 const int n = min(C::RMAX, rows_all - r0) * lines;
                 for (int k = fw * 32 + lane; k < n; k += C::FETCH * 32) {
                     const int r = r0 + k / lines, t = r / group;
-                    const uint16_t *const line =
-                        static_cast<const uint16_t *>(a.q) + ((int64_t)cb * a.T + t) * a.q_token_stride +
-                        (int64_t)(h * group + r - t * group) * a.q_head_stride + (k % lines) * 64;
-                    if (in_range(line - static_cast<const uint16_t *>(a.q), 2, q_elements(a), a.dev_status)) touch_l1(line);
+                    if constexpr (gdn::kChecked)
+                        if (!in_range(((int64_t)cb * a.T + t) * a.q_token_stride +
+                                          (int64_t)(h * group + r - t * group) * a.q_head_stride + (k % lines) * 64,
+                                      2, q_elements(a), a.dev_status))
+                            continue;
+                    touch_l1(static_cast<const uint16_t *>(a.q) + ((int64_t)cb * a.T + t) * a.q_token_stride +
+                             (int64_t)(h * group + r - t * group) * a.q_head_stride + (k % lines) * 64);
                 }
             }
             // the next place of the run (past the last one the cursor may stand anywhere)
@@ -998,8 +1001,11 @@ paged_attn_join_kernel(const GdnAttnArgs a, const int RT, const int RMAX, const 
     // part k: the first block's is its second, the others' are their first
     // (a checked build reads the first row for one that is none)
     auto at = [&](int k, int rl) {
-        const int64_t row = ((int64_t)(sp.c0 + k) * 2 + (k == 0 ? 1 : 0)) * RMAX + rl;
-        return in_range(row, 1, (int64_t)blocks * 2 * RMAX, a.dev_status) ? row : 0;
+        if constexpr (gdn::kChecked)
+            if (!in_range(((int64_t)(sp.c0 + k) * 2 + (k == 0 ? 1 : 0)) * RMAX + rl, 1, (int64_t)blocks * 2 * RMAX,
+                          a.dev_status))
+                return (int64_t)0;
+        return ((int64_t)(sp.c0 + k) * 2 + (k == 0 ? 1 : 0)) * RMAX + rl;
     };
     auto store = [&](int64_t row, int d, float4 y, float sum) {
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
