@@ -851,7 +851,17 @@ paged_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                 m[e] = base_of<C>(m[e]);        // what l and O are relative to, from here on
             }
             if constexpr (KIND == kE4M3) {
-                const float vsc = kv.v_scale ? __ldg(kv.v_scale + h) : 1.f;
+                float vsc = kv.v_scale ? __ldg(kv.v_scale + h) : 1.f;
+                // O may be 2^24 times the tokens.  Where that would take the scaled sum past the range
+                // of fp32 (scales above 2^64), the 2^15 of the weights go first, out of l too.
+                if (fabsf(vsc) > 0x1p64f) {
+                    vsc *= 0x1p-15f;
+#pragma unroll
+                    for (int e = 0; e < E; ++e) {
+                        l[e] *= 0x1p-15f;
+                        m[e] += C::UP;
+                    }
+                }
 #pragma unroll
                 for (int n = 0; n < C::DW / 8; ++n)
 #pragma unroll

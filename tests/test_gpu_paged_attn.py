@@ -359,6 +359,36 @@ def test_scores_of_any_size(gdn, dtype, cache):
         assert ((lse.cpu().double() - x * 2.0 ** power).abs() <= bound + 1e-6).all(), power
 
 
+@pytest.mark.parametrize("size", [1e-35, 1e-20, 1e20, 1e31])
+@pytest.mark.parametrize("lens", [[300] * 4, [20000]], ids=["whole", "joined"])
+def test_value_scales_of_any_size(gdn, size, lens):
+    """A power of two more in the scale is one more in the output.  (Its digits are the same where it
+    is a normal number.  Below 2^-126 bf16 has steps of 2^-133: o1 is off by 2^-9 of itself, here
+    less than 2^-135, and the output by half a step.  The sums may be taken out another power of two:
+    log2 of them, below 32, is off by an ulp, 2^-19, and its sum with the maximum by half of one.)"""
+    c = Case(36, lens, T=2, cache=E4M3)
+    (o1, l1), _ = run(gdn, c)
+    power = 2.0 ** round(math.log2(size))
+    c.v_scale = c.v_scale * power
+    o2, l2 = c.attend(gdn)
+    assert (l1 - l2).abs().max() <= 2.0 ** -17 and o2.abs().max() > 0
+    want, got = o1.double() * power, o2.double()
+    normal = want.abs() >= 2.0 ** -126
+    assert torch.equal(got[normal], want[normal]) and ((got - want).abs()[~normal] <= 2.0 ** -133).all()
+
+
+@pytest.mark.parametrize("lens", [[300] * 4, [20000]], ids=["whole", "joined"])
+def test_large_values_do_not_pass_the_range_on_the_way(gdn, lens):
+    """Values of one sign near the end of the range: their weighted sum, before it is divided by the
+    sum of the weights, would be past it."""
+    c = Case(37, lens, T=2, cache=E4M3)
+    c.v = (c.v.float().abs() + 1).to(E4M3)
+    (o1, l1), _ = run(gdn, c)
+    c.v_scale = c.v_scale * 2.0 ** 115
+    o2, l2 = c.attend(gdn)
+    assert (l1 - l2).abs().max() <= 2.0 ** -17 and torch.equal(o2.double(), o1.double() * 2.0 ** 115)
+
+
 def test_given_lse_alone_keeps_its_padding_rows(gdn):
     c = Case(31, [5, 40, 0, 7], pad=(1, 3), T=2)
     want, wl = c.attend(gdn)
